@@ -399,6 +399,142 @@ MOE_API int moe_combine(const void* ybuf, const int64_t* selected, const int64_t
                 moe_dtype dtype, int32_t* dev_status, moe_stream_t stream);
 
 /*
+ * moe_sort -- tokens sorted by expert: the dispatch without a capacity.  Every
+ * assignment i = t k + j with expert e = selected[t,j] gets a row of a packed
+ * matrix ordered by (e, t, j), so nothing is dropped and no slot stays empty
+ * ([P2] problem statement routes every token to its k experts; the pages'
+ * capacity enters in moe_dispatch only).
+ *   offsets[e]  = #{assignments to experts < e};  offsets[E] = rows in all
+ *   row[t,j]    = offsets[e] + #{earlier assignments to e}, -1 if (t,j) takes no part
+ *   source[r]   = the assignment t k + j of row r (token r's is source[r] / k),
+ *                 -1 for r >= offsets[E]
+ *   xs[r,:]     = x[source[r] / k, :]   for r < offsets[E]; other rows are not written
+ * The result is unique.  An index of -1 marks an assignment that takes no part
+ * (a padding token, a choice dropped earlier); any other index outside [0, E)
+ * sets MOE_ERR_BAD_INDEX and takes no part either.  An expert may occur twice
+ * in a token.  The gradient of xs with respect to x is moe_unsort of the
+ * rows' gradient without gates.
+ *
+ * Arguments:
+ *   selected  device int64 (T, k).
+ *   T, k, E   T >= 0 (T = 0 only clears offsets), 1 <= k <= 64, 1 <= E <= 2048, T * k < 2^30.
+ *   x         device (T, D), row stride ldx, dtype `dtype`; NULL: the order only.
+ *   offsets int32 (E + 1); row int32 (T, k); source int32 (T k): device outputs.
+ *   xs        device (T k, D), row stride ldxs, dtype `dtype`.
+ *   workspace device, >= moe_sort_workspace_size(T, k, E) bytes (which may be 0).
+ */
+MOE_API size_t moe_sort_workspace_size(int64_t T, int32_t k, int32_t E);
+MOE_API int moe_sort(const int64_t* selected, int64_t T, int32_t k, int32_t E, const void* x, moe_dtype dtype,
+                     int64_t D, int64_t ldx, int32_t* offsets, int32_t* row, int32_t* source, void* xs,
+                     int64_t ldxs, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                     moe_stream_t stream);
+
+/*
+ * moe_sort_i8 -- moe_sort whose rows are quantised on the way, as
+ * moe_quantize_i8 does it: xq[r,:] = q(x[source[r] / k]) (int8, row stride
+ * ldxq >= D; give it a multiple of 16 for moe_matmul_i8) and xscale[r] fp32
+ * (T k).  Each token is quantised once.  Columns past D of xq are not written.
+ * Other arguments, the order and the workspace as moe_sort.
+ */
+MOE_API int moe_sort_i8(const int64_t* selected, int64_t T, int32_t k, int32_t E, const void* x, moe_dtype dtype,
+                        int64_t D, int64_t ldx, int32_t* offsets, int32_t* row, int32_t* source, int8_t* xq,
+                        int64_t ldxq, float* xscale, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                        moe_stream_t stream);
+
+/*
+ * moe_unsort -- packed rows back to token order, weighted:
+ *   y[t,:] = base[t,:] + sum_{j : row[t,j] >= 0} gate[t,j] * ys[row[t,j], :]
+ * in fp32 over j ascending, rounded once; deterministic ([P2]: y = shared +
+ * sum).  A token without rows gives its base row, or zeros.  Rows of ys that
+ * no token has are not read.
+ *   ys        device (rows, N), row stride ldys, dtype `dtype`.
+ *   row       device int32 (T, k) from moe_sort: -1, or a row of ys; any other
+ *             value sets MOE_ERR_BAD_INDEX and is skipped.
+ *   gates     device (T, k) of `gate_dtype`, or NULL for all-ones (the gradient of moe_sort).
+ *   base      device (T, N), row stride ldbase, or NULL.
+ *   y         device (T, N), row stride ldy.
+ * T >= 0, k <= 64, T * k < 2^30.
+ */
+MOE_API int moe_unsort(const void* ys, int64_t ldys, int64_t rows, const int32_t* row, const void* gates,
+                       moe_dtype gate_dtype, int64_t T, int32_t k, int64_t N, const void* base, int64_t ldbase,
+                       void* y, int64_t ldy, moe_dtype dtype, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * moe_unsort_backward -- the gradients of moe_unsort for a given dy:
+ *   dys[row[t,j], :] = gate[t,j] * dy[t,:]     (rounded once; rows without a token are not written)
+ *   dgates[t,j]      = dy[t,:] . ys[row[t,j], :]   fp32 (T, k), 0 where row[t,j] < 0
+ * The gradient of base is dy itself.  Either output may be NULL to skip it;
+ * ys is read for dgates only.  No two assignments may share a row (moe_sort
+ * gives each its own): a shared row would be written twice.  row, gates and
+ * the status word as moe_unsort.
+ */
+MOE_API int moe_unsort_backward(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t rows,
+                                const int32_t* row, const void* gates, moe_dtype gate_dtype, int64_t T, int32_t k,
+                                int64_t N, void* dys, int64_t lddys, float* dgates, moe_dtype dtype,
+                                int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * moe_quantize_i8 -- rows in signed 8 bits with one scale each:
+ *   m = max_k |x[r,k]|,  scale[r] = m / 127,  q[r,k] = 127 x[r,k] / m rounded to the nearest integer
+ * (ties to even, the rounding of the exact quotient; |q| <= 127).  A row of
+ * zeros has scale 0 and q = 0.  A row with an infinity or a NaN sets
+ * MOE_ERR_NONFINITE and has scale NaN and q = 0.  Tokens (M, K) give one scale
+ * per token; weights in the (out, in) layout, taken as (E N, K), one per
+ * output channel.
+ *   x  device (M, K), row stride ldx, dtype `dtype`;  q  device int8 (M, K),
+ *   row stride ldq, columns past K not written;  scale  device fp32 (M).
+ */
+MOE_API int moe_quantize_i8(const void* x, moe_dtype dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q,
+                            int64_t ldq, float* scale, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * moe_matmul_i8 -- product of 8-bit integers with a scale per token and per
+ * output channel, dense or grouped over experts:
+ *   out[m,n] = (sum_k xq[m,k] wq[g,n,k]) * xscale[m] * wscale[g,n] (+ bias[g,n])   for offsets[g] <= m < offsets[g+1]
+ * The sum is an exact int32 on the tensor cores, scaled in fp32 and rounded
+ * once.  Rows outside [offsets[0], offsets[G]) are not written.
+ *   xq        device int8 (M, K), row stride ldx; xscale fp32 (M).
+ *   offsets   device int32 (G + 1), ascending, within [0, M] (values outside
+ *             are clamped; a group that runs backwards is empty and sets
+ *             MOE_ERR_BAD_INDEX), or NULL: G = 1 and all M rows.
+ *   wq        device int8 (G, N, K), row stride ldw (groups N ldw apart); wscale fp32 (G, N).
+ *   bias      device fp32 (G, N) or NULL.
+ *   out       device (M, N), row stride ldo, `out_dtype`.
+ *   workspace device, >= moe_matmul_i8_workspace_size(M, G, N, K) bytes, one per call in flight.
+ * xq and wq start on 16 bytes with row strides of multiples of 16 (K itself is
+ * free), else MOE_ERR_UNSUPPORTED.  G <= 2048, K <= 131071 (the int32 sum),
+ * M and G N below 2^30.  M = 0: nothing is done.
+ */
+MOE_API size_t moe_matmul_i8_workspace_size(int64_t M, int32_t G, int64_t N, int64_t K);
+MOE_API int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, int64_t ldx, const int32_t* offsets,
+                          const int8_t* wq, const float* wscale, int64_t ldw, const float* bias, int32_t G,
+                          int64_t N, int64_t K, void* out, int64_t ldo, moe_dtype out_dtype, int32_t* dev_status,
+                          void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_expert_ffn_i8 -- moe_expert_ffn on sorted rows in 8 bits: every expert
+ * applied to the rows [offsets[g], offsets[g+1]) with its weights in 8 bits
+ * (as quantised by moe_quantize_i8).  With X = xq * xscale and W = w * s:
+ *   LINEAR   : X W1^T (+ b1)                                  w1 (G, Dout, D)
+ *   GELU_MLP : q(gelu(X W1^T + b1)) W2^T (+ b2)               w1 (G, F, D), w2 (G, Dout, F)   [P5]
+ *   SWIGLU   : q(silu(X W1^T) * (X W3^T)) W2^T                w1 = gate, w3 = up (G, F, D), w2 = down (G, Dout, F)   [P3]
+ * q: the rows of the hidden activation, kept in fp32 until then, quantised as
+ * moe_quantize_i8 does.  Row strides ldw1 (w1 and w3) and ldw2; biases fp32 or
+ * NULL; ys device (M, Dout), row stride ldys, `out_dtype`; offsets, limits,
+ * alignment, rows outside the groups and the status word as moe_matmul_i8.
+ *   workspace >= moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout)
+ *   bytes on a 16-byte boundary, one per call in flight.
+ */
+MOE_API size_t moe_expert_ffn_i8_workspace_size(moe_ffn_kind kind, int32_t G, int64_t M, int64_t D, int64_t F,
+                                                int64_t Dout);
+MOE_API int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const float* xscale, int64_t M, int64_t ldx,
+                              const int32_t* offsets, int32_t G, int64_t D, int64_t F, int64_t Dout,
+                              const int8_t* w1, const float* s1, int64_t ldw1, const float* b1, const int8_t* w2,
+                              const float* s2, int64_t ldw2, const float* b2, const int8_t* w3, const float* s3,
+                              void* ys, int64_t ldys, moe_dtype out_dtype, int32_t* dev_status, void* workspace,
+                              size_t workspace_bytes, moe_stream_t stream);
+
+/*
  * moe_aux_stats -- load statistics and the Switch auxiliary loss.
  *   f[e] = counts[e] / T                         ([P2] token_fraction, sums to k)
  *   P[e] = prob_sum[e] / T                       ([P2] probability_mass, sums to 1)

@@ -11,5 +11,6 @@ from .binding import (  # noqa: F401
     moe_capacity, moe_clear_status, moe_combine, moe_dispatch, moe_dispatch_static, moe_ep_combine, moe_ep_dispatch,
     moe_ep_plan, moe_expert_ffn, moe_expert_ffn_gathered, moe_expert_ffn_save, moe_ipc_close, moe_ipc_export, moe_ipc_import,
     moe_read_status, moe_renormalize_kept_gates, moe_route, moe_router_backward, moe_transpose_weights, new_status,
+    moe_sort, moe_sort_i8, moe_unsort, moe_unsort_backward, moe_quantize_i8, moe_matmul_i8, moe_expert_ffn_i8,
     status_string, moe_swiglu_layer_forward, moe_swiglu_layer_workspace_size, SwiGLULayerDesc,
 )

@@ -9,6 +9,7 @@ this module's functions raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -41,7 +42,9 @@ EXPORTED = [
     "moe_backward_swiglu", "moe_router_backward_workspace_size", "moe_router_backward",
     "moe_backward_gelu_workspace_size", "moe_backward_gelu", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine",
     "moe_ipc_export", "moe_ipc_import", "moe_ipc_close", "moe_expert_ffn_save", "moe_wait_probe",
-    "moe_swiglu_layer_workspace_size", "moe_swiglu_layer_forward",
+    "moe_swiglu_layer_workspace_size", "moe_swiglu_layer_forward", "moe_sort_workspace_size", "moe_sort", "moe_sort_i8",
+    "moe_unsort", "moe_unsort_backward", "moe_quantize_i8", "moe_matmul_i8_workspace_size", "moe_matmul_i8",
+    "moe_expert_ffn_i8_workspace_size", "moe_expert_ffn_i8",
 ]
 IPC_HANDLE_BYTES = 64
 SCORING = {"softmax": 0, "sigmoid": 1}
@@ -141,6 +144,26 @@ def lib():
         L.moe_swiglu_layer_workspace_size.argtypes = [ctypes.POINTER(SwiGLULayerDesc)]
         L.moe_swiglu_layer_forward.argtypes = [ctypes.POINTER(SwiGLULayerDesc), _vp, _vp, _vp, _vp, _vp, _sz, _vp,
                                                _vp, _vp, _vp, _vp, _vp]
+        L.moe_sort_workspace_size.restype = _sz
+        L.moe_sort_workspace_size.argtypes = [_i64, _i32, _i32]
+        L.moe_sort.argtypes = [_vp, _i64, _i32, _i32, _vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
+                               _vp, _sz, _vp]
+        L.moe_sort_i8.argtypes = [_vp, _i64, _i32, _i32, _vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _i64,
+                                  _vp, _vp, _vp, _sz, _vp]
+        L.moe_unsort.argtypes = [_vp, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _i32, _i64, _vp, _i64, _vp, _i64,
+                                 ctypes.c_int, _vp, _vp]
+        L.moe_unsort_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _i32, _i64, _vp,
+                                          _i64, _vp, ctypes.c_int, _vp, _vp]
+        L.moe_quantize_i8.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
+        L.moe_matmul_i8_workspace_size.restype = _sz
+        L.moe_matmul_i8_workspace_size.argtypes = [_i64, _i32, _i64, _i64]
+        L.moe_matmul_i8.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _i64,
+                                    ctypes.c_int, _vp, _vp, _sz, _vp]
+        L.moe_expert_ffn_i8_workspace_size.restype = _sz
+        L.moe_expert_ffn_i8_workspace_size.argtypes = [ctypes.c_int, _i32, _i64, _i64, _i64, _i64]
+        L.moe_expert_ffn_i8.argtypes = [ctypes.c_int, _vp, _vp, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64,
+                                        _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, _sz,
+                                        _vp]
         L.moe_clear_status.argtypes = [_vp, _vp]
         L.moe_read_status.argtypes = [_vp, _vp, ctypes.POINTER(_i32)]
         _lib = L
@@ -691,6 +714,475 @@ def moe_swiglu_layer_forward(desc: SwiGLULayerDesc, x: torch.Tensor, y: torch.Te
                                         st(copy_out_stream), ev(x_free), ev(y_free))
     _check("moe_swiglu_layer_forward", rc)
     return y
+
+
+# ------------------------------------------------------------------------------
+# Sorted rows and 8-bit products.  These calls run on the device of their tensors, whichever is current, and allocate on
+# the stream they launch on (``stream``, or that device's current one).  They take tensors as they are or refuse them:
+# nothing is copied behind the caller's back.
+@contextlib.contextmanager
+def _launching(dev: torch.device, stream):
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch._C._cuda_getCurrentRawStream(dev.index), None
+        else:
+            if stream.device != dev:
+                raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+            caller = torch.cuda.current_stream(dev)
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream, caller
+
+
+class _Here:
+    """The launch on the current device's current stream (no context to enter)."""
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw, None
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _launch(dev: torch.device, stream):
+    """Context giving (raw stream, the caller's stream if another one)."""
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
+    return _launching(dev, stream)
+
+
+def _take(name: str, t: torch.Tensor, dev: torch.device, dtype=None, shape=None, contiguous: bool = False):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a tensor on a CUDA device")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _ld(name: str, t: torch.Tensor, unit: int = 1) -> int:
+    """Row stride of a 2-D tensor with unit column stride; a single row's is rounded up to ``unit``."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows <= 1:
+        return -(-max(cols, 1) // unit) * unit
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.stride(0)
+
+
+def _status(dev_status, dev):
+    if dev_status is not None:
+        _take("dev_status", dev_status, dev, torch.int32, contiguous=True)
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status is empty")
+    return _p(dev_status)
+
+
+def _scratch(nbytes: int, dev, ws):
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _take("workspace", ws, dev, contiguous=True)
+    if ws.numel() * ws.element_size() < nbytes:
+        raise ValueError(f"workspace holds {ws.numel() * ws.element_size()} bytes, needs {nbytes}")
+    return ws
+
+
+def _nbytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _keep(caller, *tensors):
+    """Outputs made on another stream: the allocator waits for the caller's stream too before it reuses them."""
+    if caller is not None:
+        for t in tensors:
+            t.record_stream(caller)
+
+
+def _out(o: dict, name: str, shape, dtype, dev, fresh: list):
+    """o[name] if given (checked), else a new tensor."""
+    t = o.get(name)
+    if t is None:
+        t = o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        fresh.append(t)
+    else:
+        _take(name, t, dev, dtype, shape, contiguous=True)
+    return t
+
+
+def _padded(rows_shape, K: int, dev) -> torch.Tensor:
+    """int8 (*rows_shape, K) whose rows start on multiples of 16 bytes."""
+    return torch.empty(*rows_shape, -(-K // 16) * 16, dtype=torch.int8, device=dev)[..., :K]
+
+
+def moe_sort_workspace_size(T: int, k: int, E: int) -> int:
+    return int(lib().moe_sort_workspace_size(T, k, E))
+
+
+def _sort_args(selected, E):
+    dev = _dev(selected)
+    if selected.dtype != torch.int64:
+        raise TypeError("selected must be int64")
+    if selected.dim() not in (1, 2) or not selected.is_contiguous():
+        raise ValueError("selected must be a contiguous (T,) or (T, k) tensor")
+    T, k = selected.shape if selected.dim() == 2 else (selected.shape[0], 1)
+    if E < 1:
+        raise ValueError("E must be positive")
+    return dev, T, k
+
+
+def moe_sort(selected: torch.Tensor, E: int, x: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+             dev_status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Tokens sorted by expert, without a capacity: the packed rows of every assignment, ordered by (expert, t, j).
+
+    ``selected`` int64 (T, k) (-1: takes no part); ``x`` (T, D) or None for the order only.
+    Returns offsets int32 (E+1), row int32 (T, k) (-1: none), source int32 (T*k) (the assignment of each row, -1 behind the
+    last) and, with x, xs (T*k, D), whose rows from offsets[E] on are not written.  Gradient of x: ``moe_unsort`` of the rows'
+    gradient with gates=None.
+    """
+    dev, T, k = _sort_args(selected, E)
+    dt, D, ldx, ldxs = MOE_F32, 0, 0, 0
+    if x is not None:
+        _take("x", x, dev)
+        if x.dim() != 2 or x.shape[0] != T:
+            raise ValueError("x must be (T, D)")
+        dt, D, ldx = _dt(x), x.shape[1], _ld("x", x)
+    o = {} if out is None else dict(out)
+    fresh = []
+    with _launch(dev, stream) as (raw, caller):
+        offsets = _out(o, "offsets", (E + 1,), torch.int32, dev, fresh)
+        row = _out(o, "row", (T, k), torch.int32, dev, fresh)
+        source = _out(o, "source", (T * k,), torch.int32, dev, fresh)
+        xs = None
+        if x is not None:
+            xs = o.get("xs")
+            if xs is None:
+                xs = _out(o, "xs", (T * k, D), x.dtype, dev, fresh)
+            else:
+                _take("xs", xs, dev, x.dtype, (T * k, D))
+            ldxs = _ld("xs", xs)
+        ws = _scratch(moe_sort_workspace_size(T, k, E), dev, workspace)
+        rc = lib().moe_sort(_p(selected), T, k, E, _p(x), dt, D, ldx, _p(offsets), _p(row), _p(source), _p(xs), ldxs,
+                            _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        _check("moe_sort", rc)
+        _keep(caller, *fresh)
+    return o
+
+
+def moe_sort_i8(selected: torch.Tensor, E: int, x: torch.Tensor, out: Optional[dict] = None,
+                dev_status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> dict:
+    """``moe_sort`` with the rows quantised on the way: xq int8 (T*k, D) (rows on multiples of 16 bytes) and
+    xscale fp32 (T*k) in place of xs."""
+    dev, T, k = _sort_args(selected, E)
+    _take("x", x, dev)
+    if x.dim() != 2 or x.shape[0] != T:
+        raise ValueError("x must be (T, D)")
+    dt, D, ldx = _dt(x), x.shape[1], _ld("x", x)
+    o = {} if out is None else dict(out)
+    fresh = []
+    with _launch(dev, stream) as (raw, caller):
+        offsets = _out(o, "offsets", (E + 1,), torch.int32, dev, fresh)
+        row = _out(o, "row", (T, k), torch.int32, dev, fresh)
+        source = _out(o, "source", (T * k,), torch.int32, dev, fresh)
+        xscale = _out(o, "xscale", (T * k,), torch.float32, dev, fresh)
+        xq = o.get("xq")
+        if xq is None:
+            xq = o["xq"] = _padded((T * k,), D, dev)
+            fresh.append(xq)
+        else:
+            _take("xq", xq, dev, torch.int8, (T * k, D))
+        ws = _scratch(moe_sort_workspace_size(T, k, E), dev, workspace)
+        rc = lib().moe_sort_i8(_p(selected), T, k, E, _p(x), dt, D, ldx, _p(offsets), _p(row), _p(source), _p(xq),
+                               _ld("xq", xq), _p(xscale), _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        _check("moe_sort_i8", rc)
+        _keep(caller, *fresh)
+    return o
+
+
+def _gates(gates, dev, T, k):
+    if gates is None:
+        return None, MOE_F32
+    _take("gates", gates, dev, shape=(T, k), contiguous=True)
+    return _p(gates), _dt(gates)
+
+
+def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor] = None,
+               base: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = base[t] + sum_j gates[t, j] * ys[row[t, j]] over row >= 0 (fixed j order, fp32 accumulation).
+
+    ``ys`` (rows, N); ``row`` int32 (T, k) from ``moe_sort``; without gates the sum is the gradient of ``moe_sort``.
+    """
+    dev = _dev(ys)
+    if ys.dim() != 2:
+        raise ValueError("ys must be (rows, N)")
+    dt, (R, N) = _dt(ys), ys.shape
+    _take("row", row, dev, torch.int32, contiguous=True)
+    if row.dim() != 2:
+        raise ValueError("row must be (T, k)")
+    T, k = row.shape
+    g, gdt = _gates(gates, dev, T, k)
+    ldb = 0
+    if base is not None:
+        ldb = _ld("base", _take("base", base, dev, ys.dtype, (T, N)))
+    with _launch(dev, stream) as (raw, caller):
+        if y is None:
+            y = torch.empty(T, N, dtype=ys.dtype, device=dev)
+            _keep(caller, y)
+        else:
+            _take("y", y, dev, ys.dtype, (T, N))
+        rc = lib().moe_unsort(_p(ys), _ld("ys", ys), R, _p(row), g, gdt, T, k, N, _p(base), ldb, _p(y), _ld("y", y), dt,
+                              _status(dev_status, dev), raw)
+        _check("moe_unsort", rc)
+    return y
+
+
+def moe_unsort_backward(dy: torch.Tensor, ys: Optional[torch.Tensor], row: torch.Tensor,
+                        gates: Optional[torch.Tensor] = None, rows: Optional[int] = None, want_dys: bool = True,
+                        want_dgates: bool = True, dys: Optional[torch.Tensor] = None,
+                        dgates: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of ``moe_unsort``: (dys (rows, N) in dy's dtype, dgates fp32 (T, k)); the base's is dy.
+
+    ``ys`` is read for dgates only; without it pass want_dgates=False and ``rows``.  Rows of dys that no assignment has are
+    not written.
+    """
+    dev = _dev(dy)
+    _take("row", row, dev, torch.int32, contiguous=True)
+    if row.dim() != 2 or dy.dim() != 2 or dy.shape[0] != row.shape[0]:
+        raise ValueError("row must be (T, k) and dy (T, N)")
+    (T, k), N, dt = row.shape, dy.shape[1], _dt(dy)
+    if ys is not None:
+        if ys.dim() != 2 or ys.shape[1] != N:
+            raise ValueError("ys must be (rows, N)")
+        _take("ys", ys, dev, dy.dtype)
+        if rows is not None and rows != ys.shape[0]:
+            raise ValueError("rows differs from ys's")
+        rows = ys.shape[0]
+    elif want_dgates:
+        raise ValueError("dgates needs ys")
+    elif rows is None:
+        rows = T * k if dys is None else dys.shape[0]
+    g, gdt = _gates(gates, dev, T, k)
+    with _launch(dev, stream) as (raw, caller):
+        fresh = []
+        if not want_dys:
+            dys = None
+        elif dys is None:
+            dys = torch.empty(rows, N, dtype=dy.dtype, device=dev)
+            fresh.append(dys)
+        else:
+            _take("dys", dys, dev, dy.dtype, (rows, N))
+        if not want_dgates:
+            dgates = None
+        elif dgates is None:
+            dgates = torch.empty(T, k, dtype=torch.float32, device=dev)
+            fresh.append(dgates)
+        else:
+            _take("dgates", dgates, dev, torch.float32, (T, k), contiguous=True)
+        rc = lib().moe_unsort_backward(_p(dy), _ld("dy", dy), _p(ys), 0 if ys is None else _ld("ys", ys), rows, _p(row), g,
+                                       gdt, T, k, N, _p(dys), 0 if dys is None else _ld("dys", dys), _p(dgates), dt,
+                                       _status(dev_status, dev), raw)
+        _check("moe_unsort_backward", rc)
+        _keep(caller, *fresh)
+    return dys, dgates
+
+
+def moe_quantize_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                    dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Rows of x (..., K) in 8 bits: (q int8 (..., K), scale fp32 (...)), one scale per row.
+
+    Tokens (M, K) give a scale per token, weights (E, N, K) one per output channel.  A new q has its rows on multiples of 16
+    bytes, as ``moe_matmul_i8`` takes them.  x beyond two dimensions must be contiguous.
+    """
+    dev = _dev(x)
+    if x.dim() < 2:
+        raise ValueError("x must be (..., K)")
+    if x.dim() > 2 and not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    lead, K, dt = tuple(x.shape[:-1]), x.shape[-1], _dt(x)
+    x2 = x if x.dim() == 2 else x.view(-1, K)
+    M = x2.shape[0]
+    with _launch(dev, stream) as (raw, caller):
+        fresh = []
+        if q is None:
+            q = _padded(lead, K, dev)
+            fresh.append(q)
+        else:
+            _take("q", q, dev, torch.int8, x.shape)
+        if scale is None:
+            scale = torch.empty(lead, dtype=torch.float32, device=dev)
+            fresh.append(scale)
+        else:
+            _take("scale", scale, dev, torch.float32, lead, contiguous=True)
+        ldq = _ld3("q", q, 1)
+        rc = lib().moe_quantize_i8(_p(x), dt, M, K, _ld("x", x2), _p(q), ldq, _p(scale), _status(dev_status, dev), raw)
+        _check("moe_quantize_i8", rc)
+        _keep(caller, *fresh)
+    return q, scale
+
+
+def _ld3(name: str, t: torch.Tensor, unit: int) -> int:
+    """The one row stride of a tensor (..., N, K) whose rows lie evenly; a single row's is rounded up to ``unit``."""
+    if t.dim() == 2:
+        return _ld(name, t, unit)
+    K = t.shape[-1]
+    if K > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld, rows = None, 1
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] > 1:
+            if ld is None:
+                if t.stride(d) % rows:
+                    raise ValueError(f"{name}'s rows are not evenly spaced")
+                ld = t.stride(d) // rows
+            elif t.stride(d) != ld * rows:
+                raise ValueError(f"{name}'s rows are not evenly spaced")
+        rows *= t.shape[d]
+    if ld is None:
+        return -(-max(K, 1) // unit) * unit
+    if ld < K:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+def _weight_i8(name, w, scale, dev, G, N, K):
+    """Checks an 8-bit weight (G, N, K) or, for G = 1, (N, K) with its scales; returns the row stride."""
+    _take(name, w, dev, torch.int8)
+    if tuple(w.shape) not in ((G, N, K), (N, K) if G == 1 else (G, N, K)):
+        raise ValueError(f"{name} must be ({G}, {N}, {K}), got {tuple(w.shape)}")
+    _take(f"{name}'s scale", scale, dev, torch.float32, contiguous=True)
+    if scale.numel() != G * N:
+        raise ValueError(f"{name} needs {G * N} scales, got {scale.numel()}")
+    return _ld3(name, w, 16)
+
+
+def _rows_i8(xq, xscale, offsets):
+    dev = _dev(xq)
+    if xq.dim() != 2:
+        raise ValueError("xq must be (M, K)")
+    _take("xq", xq, dev, torch.int8)
+    M, K = xq.shape
+    _take("xscale", xscale, dev, torch.float32, (M,), contiguous=True)
+    if offsets is not None:
+        _take("offsets", offsets, dev, torch.int32, contiguous=True)
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets must be (G + 1,)")
+    return dev, M, K, 1 if offsets is None else offsets.shape[0] - 1
+
+
+def _bias_i8(name, b, dev, G, N):
+    if b is not None:
+        _take(name, b, dev, torch.float32, contiguous=True)
+        if b.numel() != G * N:
+            raise ValueError(f"{name} must hold {G * N} values")
+    return _p(b)
+
+
+def _out_dt(out, out_dtype):
+    dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    if out is not None and out_dtype is not None and out_dtype != dtype:
+        raise TypeError("out_dtype differs from the output's")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dtype}; expected float32 or bfloat16")
+    return dtype, MOE_F32 if dtype == torch.float32 else MOE_BF16
+
+
+def moe_matmul_i8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wscale: torch.Tensor,
+                  offsets: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                  dev_status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """out[m] = (xq[m] . wq[g]^T) * xscale[m] * wscale[g] (+ bias[g]), exact integer sums; bf16 unless out_dtype says fp32.
+
+    ``xq`` int8 (M, K) and ``wq`` int8 (G, N, K) as ``moe_quantize_i8`` gives them; with ``offsets`` int32 (G+1) the rows
+    [offsets[g], offsets[g+1]) take weight g (rows outside are not written), without it G = 1.
+    """
+    dev, M, K, G = _rows_i8(xq, xscale, offsets)
+    if wq.dim() not in (2, 3):
+        raise ValueError("wq must be (G, N, K)")
+    N = wq.shape[-2]
+    ldw = _weight_i8("wq", wq, wscale, dev, G, N, K)
+    b = _bias_i8("bias", bias, dev, G, N)
+    dtype, dt = _out_dt(out, out_dtype)
+    with _launch(dev, stream) as (raw, caller):
+        if out is None:
+            out = torch.empty(M, N, dtype=dtype, device=dev)
+            _keep(caller, out)
+        else:
+            _take("out", out, dev, dtype, (M, N))
+        ws = _scratch(int(lib().moe_matmul_i8_workspace_size(M, G, N, K)), dev, workspace)
+        rc = lib().moe_matmul_i8(_p(xq), _p(xscale), M, _ld("xq", xq, 16), _p(offsets), _p(wq), _p(wscale), ldw, b, G, N, K,
+                                 _p(out), _ld("out", out), dt, _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        _check("moe_matmul_i8", rc)
+    return out
+
+
+def moe_matmul_i8_workspace_size(M: int, G: int, N: int, K: int) -> int:
+    return int(lib().moe_matmul_i8_workspace_size(M, G, N, K))
+
+
+def moe_expert_ffn_i8_workspace_size(kind: str, G: int, M: int, D: int, F: int, Dout: int) -> int:
+    return int(lib().moe_expert_ffn_i8_workspace_size(FFN[kind], G, M, D, F, Dout))
+
+
+def moe_expert_ffn_i8(kind: str, xq: torch.Tensor, xscale: torch.Tensor, offsets: Optional[torch.Tensor],
+                      w1: torch.Tensor, s1: torch.Tensor, b1: Optional[torch.Tensor] = None,
+                      w2: Optional[torch.Tensor] = None, s2: Optional[torch.Tensor] = None,
+                      b2: Optional[torch.Tensor] = None, w3: Optional[torch.Tensor] = None,
+                      s3: Optional[torch.Tensor] = None, ys: Optional[torch.Tensor] = None,
+                      out_dtype: Optional[torch.dtype] = None, dev_status: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Grouped expert FFN on sorted rows in 8 bits (kinds as ``moe_expert_ffn``); returns ys (M, Dout).
+
+    ``xq``, ``xscale`` and ``offsets`` from ``moe_sort_i8``; weights int8 (G, out, in) with one scale per output channel
+    from ``moe_quantize_i8`` (swiglu: w1 = gate, w3 = up, w2 = down); biases fp32 (G, out).  The hidden rows are quantised
+    from fp32 between the two products.
+    """
+    if kind not in FFN:
+        raise ValueError(f"unknown kind {kind!r}; known: {sorted(FFN)}")
+    dev, M, D, G = _rows_i8(xq, xscale, offsets)
+    n1 = w1.shape[-2] if w1.dim() in (2, 3) else 0
+    ld1 = _weight_i8("w1", w1, s1, dev, G, n1, D)
+    F, Dout, ld2 = 0, n1, 0
+    if kind == "linear":
+        if any(t is not None for t in (w2, s2, b2, w3, s3)):
+            raise ValueError("linear experts take w1, s1 and b1 only")
+    else:
+        F = n1
+        if w2 is None or w2.dim() not in (2, 3):
+            raise ValueError("w2 must be (G, Dout, F)")
+        Dout = w2.shape[-2]
+        ld2 = _weight_i8("w2", w2, s2, dev, G, Dout, F)
+    if kind == "swiglu":
+        if b1 is not None or b2 is not None:
+            raise ValueError("SwiGLU experts take no biases")
+        if _weight_i8("w3", w3, s3, dev, G, F, D) != ld1 and G * F > 1:
+            raise ValueError("w1 and w3 must have the same row stride")
+    elif w3 is not None or s3 is not None:
+        raise ValueError("w3 belongs to SwiGLU experts")
+    pb1, pb2 = _bias_i8("b1", b1, dev, G, n1), _bias_i8("b2", b2, dev, G, Dout)
+    dtype, dt = _out_dt(ys, out_dtype)
+    with _launch(dev, stream) as (raw, caller):
+        if ys is None:
+            ys = torch.empty(M, Dout, dtype=dtype, device=dev)
+            _keep(caller, ys)
+        else:
+            _take("ys", ys, dev, dtype, (M, Dout))
+        ws = _scratch(moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout), dev, workspace)
+        rc = lib().moe_expert_ffn_i8(FFN[kind], _p(xq), _p(xscale), M, _ld("xq", xq, 16), _p(offsets), G, D, F, Dout,
+                                     _p(w1), _p(s1), ld1, pb1, _p(w2), _p(s2), ld2, pb2, _p(w3), _p(s3), _p(ys),
+                                     _ld("ys", ys), dt, _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        _check("moe_expert_ffn_i8", rc)
+    return ys
 
 
 def moe_wait_probe(flag: torch.Tensor, limit_ns: int, dev_status: torch.Tensor, stream=None):

@@ -1,0 +1,44 @@
+// Grouped product of 8-bit integers on the tensor cores (see i8_gemm.cu) and the row quantisation before it.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+enum I8Epilogue : int {
+    I8_OUT = 0,    // out = acc xscale wscale (+ bias)
+    I8_GELU = 1,   // out = gelu(acc xscale wscale (+ bias))
+    I8_SWIGLU = 2  // two weights: out = silu(acc_gate ...) (acc_up ...)
+};
+
+struct I8Problem {
+    const int8_t* x;       // (M, K), row stride ldx
+    const float* xscale;   // (M)
+    int64_t M, ldx;
+    const int32_t* offsets;  // device (G + 1), or NULL: G = 1 and all M rows
+    const int8_t* w;       // (G, N, K), row stride ldw
+    const float* wscale;   // (G, N)
+    const int8_t* w2;      // I8_SWIGLU: the up projection, laid out as w
+    const float* wscale2;
+    int64_t ldw;
+    const float* bias;     // (G, N) or NULL; not with I8_SWIGLU
+    int G;
+    int64_t N, K;
+    void* out;             // (M, N), row stride ldo
+    int64_t ldo;
+    moe_dtype out_dtype;
+    int epilogue;
+    uint32_t* tile_counter;  // one device word of scratch (zeroed by the call, in stream order)
+    int32_t* status;
+};
+
+// Checks sizes and alignment, encodes the tensor maps and launches.  Returns a moe_status.
+int i8_gemm_run(const I8Problem& p, cudaStream_t stream);
+
+// Rows of x in 8 bits: all M, or with offsets (G + 1, device) those in [offsets[0], offsets[G]).
+int quantize_rows(const void* x, moe_dtype dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq,
+                  float* scale, const int32_t* offsets, int G, int32_t* status, cudaStream_t stream);
+
+}  // namespace moe
