@@ -292,31 +292,23 @@ int sort_run(SortParams p, int op, moe_dtype dtype, void* workspace, size_t work
 
 // ------------------------------- and back -----------------------------------
 
-// 16 bytes, or one element, as fp32 values
-template <typename T, int N>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[N]) {
-    if constexpr (N == 1) {
-        v[0] = to_f32(*p);
-    } else {
-        const uint4 r = *reinterpret_cast<const uint4*>(p);
+// V: 16 bytes, or one element, of a row of T; its values as fp32
+template <typename T, typename V>
+struct Vec {
+    static constexpr int kN = sizeof(V) / sizeof(T);
+    static __device__ __forceinline__ void unpack(const V& r, float (&v)[kN]) {
         const T* e = reinterpret_cast<const T*>(&r);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = to_f32(e[i]);
+        for (int i = 0; i < kN; ++i) v[i] = to_f32(e[i]);
     }
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
-    if constexpr (N == 1) {
-        *p = from_f32<T>(v[0]);
-    } else {
-        uint4 r;
+    static __device__ __forceinline__ V pack(const float (&v)[kN]) {
+        V r;
         T* e = reinterpret_cast<T*>(&r);
 #pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = from_f32<T>(v[i]);
-        *reinterpret_cast<uint4*>(p) = r;
+        for (int i = 0; i < kN; ++i) e[i] = from_f32<T>(v[i]);
+        return r;
     }
-}
+};
 
 struct UnsortParams {
     const void* ys;
@@ -333,6 +325,7 @@ struct UnsortParams {
     const void* dy;
     int64_t lddy;
     float* dgates;
+    int split;          // moe_unsort: warps per token
     int32_t* status;
 };
 
@@ -364,104 +357,157 @@ __device__ __forceinline__ int token_rows(const UnsortParams& p, int64_t t, int 
     return n;
 }
 
-// y[t] = base[t] + sum_j gate ys[row], j ascending, in fp32.  One warp per token; kBatch rows in flight per lane.
-template <typename T, typename G, int N>
+// acc[u] += sum over the J rows from j on, in their order: J x U loads in flight
+template <typename T, typename V, int J, int U>
+__device__ __forceinline__ void add_rows(const T* ys, int64_t ldys, const int* s_row, const float* s_gate, int j,
+                                         const int64_t (&col)[U], float (&acc)[U][Vec<T, V>::kN]) {
+    V r[J][U];
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+        const T* src = ys + (int64_t)s_row[j + i] * ldys;
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[i][u] = *reinterpret_cast<const V*>(src + col[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+        const float g = s_gate[j + i];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[Vec<T, V>::kN];
+            Vec<T, V>::unpack(r[i][u], v);
+#pragma unroll
+            for (int e = 0; e < Vec<T, V>::kN; ++e) acc[u][e] = fmaf(g, v[e], acc[u][e]);
+        }
+    }
+}
+
+// y[t] = base[t] + sum_j gate ys[row], j ascending, in fp32.  `split` warps share a token's columns; a warp takes U
+// vectors per lane at a time and J rows, so that J x U loads are in flight: without that the rows come one latency
+// after another.
+template <typename T, typename G, typename V, int J, int U>
 __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) {
-    constexpr int kBatch = 8;
+    constexpr int N = Vec<T, V>::kN;
     __shared__ int s_row[kWarps][kMaxK];
     __shared__ float s_gate[kWarps][kMaxK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
+    const int64_t t = unit / p.split;
     if (t >= p.T) return;
     const int n = token_rows<G>(p, t, lane, s_row[warp], s_gate[warp]);
     const T* ys = static_cast<const T*>(p.ys);
     const T* base = p.base ? static_cast<const T*>(p.base) + t * p.ldbase : nullptr;
     T* y = static_cast<T*>(p.y) + t * p.ldy;
-    for (int64_t c = (int64_t)lane * N; c < p.N; c += 32 * N) {
-        float acc[N];
+    for (int64_t c0 = (unit - t * p.split) * (32 * N * U); c0 < p.N; c0 += (int64_t)p.split * (32 * N * U)) {
+        int64_t col[U];
+        float acc[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + 32 * N * u + lane * N;
+            col[u] = c < p.N ? c : p.N - N;  // past the end: the last vector again, not stored
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[u][e] = 0.f;
+        }
         if (base) {
-            load_vec<T, N>(base + c, acc);
-        } else {
+            V r[U];
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = 0.f;
+            for (int u = 0; u < U; ++u) r[u] = *reinterpret_cast<const V*>(base + col[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) Vec<T, V>::unpack(r[u], acc[u]);
         }
-        for (int j0 = 0; j0 < n; j0 += kBatch) {
-            float v[kBatch][N];
+        int j = 0;
+        for (; n - j >= J; j += J) add_rows<T, V, J, U>(ys, p.ldys, s_row[warp], s_gate[warp], j, col, acc);
+        if (J > 4 && n - j >= 4) add_rows<T, V, 4, U>(ys, p.ldys, s_row[warp], s_gate[warp], j, col, acc), j += 4;
+        if (J > 2 && n - j >= 2) add_rows<T, V, 2, U>(ys, p.ldys, s_row[warp], s_gate[warp], j, col, acc), j += 2;
+        if (n - j >= 1) add_rows<T, V, 1, U>(ys, p.ldys, s_row[warp], s_gate[warp], j, col, acc);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (j0 + u < n) load_vec<T, N>(ys + (int64_t)s_row[warp][j0 + u] * p.ldys + c, v[u]);
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (j0 + u < n) {
-                    const float g = s_gate[warp][j0 + u];
-#pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i] = fmaf(g, v[u][i], acc[i]);
-                }
-        }
-        store_vec<T, N>(y + c, acc);
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * N * u + lane * N < p.N) *reinterpret_cast<V*>(y + col[u]) = Vec<T, V>::pack(acc[u]);
     }
 }
 
-// dys[row] = gate dy[t] and dgates[t, j] = dy[t] . ys[row], one warp per token: dy's row is read once from
-// memory and then from the first-level cache for each j.
-template <typename T, typename G, int N, bool DYS, bool DGATES>
+// dys[row] = gate dy[t] and dgates[t, j] = dy[t] . ys[row], one warp per (t, j).  The warps of a token sit in one
+// block, so that dy's row comes from memory once and from the first-level cache after that.
+template <typename T, typename G, typename V, int U, bool DYS, bool DGATES>
 __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const UnsortParams p) {
-    constexpr int kBatch = 4;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-    if (t >= p.T) return;
-    const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
-    for (int j = 0; j < p.k; ++j) {
-        const int64_t r = p.row[t * p.k + j];
-        float dot = 0.f;
-        if (r >= 0 && r < p.rows) {
-            const float g = p.gates ? to_f32(static_cast<const G*>(p.gates)[t * p.k + j]) : 1.f;
-            const T* ys = static_cast<const T*>(p.ys) + r * p.ldys;
-            T* dys = static_cast<T*>(p.y) + r * p.ldy;
-            for (int64_t c0 = (int64_t)lane * N; c0 < p.N; c0 += 32 * N * kBatch) {
-                float d[kBatch][N], v[kBatch][N];
+    constexpr int N = Vec<T, V>::kN;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit >= p.T * p.k) return;
+    const int64_t t = unit / p.k;
+    const int64_t r = p.row[unit];
+    float dot = 0.f;
+    if (r >= 0 && r < p.rows) {
+        const float g = p.gates ? to_f32(static_cast<const G*>(p.gates)[unit]) : 1.f;
+        const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
+        const T* ys = static_cast<const T*>(p.ys) + r * p.ldys;
+        T* dys = static_cast<T*>(p.y) + r * p.ldy;
+        for (int64_t c0 = 0; c0 < p.N; c0 += 32 * N * U) {
+            V a[U], b[U];
+            int64_t col[U];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int64_t c = c0 + 32 * N * u;
-                    if (c < p.N) {
-                        load_vec<T, N>(dy + c, d[u]);
-                        if (DGATES) load_vec<T, N>(ys + c, v[u]);
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + 32 * N * u + lane * N;
+                col[u] = c < p.N ? c : p.N - N;
+                a[u] = *reinterpret_cast<const V*>(dy + col[u]);
+                if (DGATES) b[u] = *reinterpret_cast<const V*>(ys + col[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float d[N];
+                Vec<T, V>::unpack(a[u], d);
+                const bool in = c0 + 32 * N * u + lane * N < p.N;
+                if (DGATES) {
+                    float v[N];
+                    Vec<T, V>::unpack(b[u], v);
+                    if (in) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) dot = fmaf(d[e], v[e], dot);
                     }
                 }
+                if (DYS && in) {
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int64_t c = c0 + 32 * N * u;
-                    if (c < p.N) {
-                        if (DGATES) {
-#pragma unroll
-                            for (int i = 0; i < N; ++i) dot = fmaf(d[u][i], v[u][i], dot);
-                        }
-                        if (DYS) {
-#pragma unroll
-                            for (int i = 0; i < N; ++i) d[u][i] *= g;
-                            store_vec<T, N>(dys + c, d[u]);
-                        }
-                    }
+                    for (int e = 0; e < N; ++e) d[e] *= g;
+                    *reinterpret_cast<V*>(dys + col[u]) = Vec<T, V>::pack(d);
                 }
             }
-        } else if (r != -1 && lane == 0) {
-            set_status(p.status, MOE_ERR_BAD_INDEX);
         }
-        if (DGATES) {
-            dot = warp_sum(dot);
-            if (lane == 0) p.dgates[t * p.k + j] = dot;
-        }
+    } else if (r != -1 && lane == 0) {
+        set_status(p.status, MOE_ERR_BAD_INDEX);
+    }
+    if (DGATES) {
+        dot = warp_sum(dot);
+        if (lane == 0) p.dgates[unit] = dot;
     }
 }
 
-template <typename T, typename G, int N>
-int launch_unsort(const UnsortParams& p, bool backward, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((p.T + kWarps - 1) / kWarps);
-    if (!backward) unsort_kernel<T, G, N><<<grid, kThreads, 0, stream>>>(p);
-    else if (p.y && p.dgates) unsort_backward_kernel<T, G, N, true, true><<<grid, kThreads, 0, stream>>>(p);
-    else if (p.y) unsort_backward_kernel<T, G, N, true, false><<<grid, kThreads, 0, stream>>>(p);
-    else unsort_backward_kernel<T, G, N, false, true><<<grid, kThreads, 0, stream>>>(p);
+constexpr int kFill = 16;  // warps per SM that a short batch is spread over
+
+template <typename T, typename G, typename V, int J, int U>
+int launch_unsort(UnsortParams p, cudaStream_t stream) {
+    const int64_t groups = (p.N + 32 * Vec<T, V>::kN * U - 1) / (32 * Vec<T, V>::kN * U);
+    const int64_t want = (int64_t)device_sm_count() * kFill / p.T;
+    p.split = (int)(want < 1 ? 1 : want < groups ? want : groups);
+    const int64_t grid = (p.T * p.split + kWarps - 1) / kWarps;
+    unsort_kernel<T, G, V, J, U><<<(unsigned)grid, kThreads, 0, stream>>>(p);
     return launch_status();
+}
+
+template <typename T, typename G, typename V, int U>
+int launch_backward(const UnsortParams& p, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((p.T * p.k + kWarps - 1) / kWarps);
+    if (p.y && p.dgates) unsort_backward_kernel<T, G, V, U, true, true><<<grid, kThreads, 0, stream>>>(p);
+    else if (p.y) unsort_backward_kernel<T, G, V, U, true, false><<<grid, kThreads, 0, stream>>>(p);
+    else unsort_backward_kernel<T, G, V, U, false, true><<<grid, kThreads, 0, stream>>>(p);
+    return launch_status();
+}
+
+// Rows that 16 bytes divide, or single elements (two loads for each of the 16-byte form's).
+template <typename T, typename G>
+int launch_back(const UnsortParams& p, bool backward, bool vec, cudaStream_t stream) {
+    if (backward) return vec ? launch_backward<T, G, uint4, 4>(p, stream) : launch_backward<T, G, T, 8>(p, stream);
+    if (p.k >= 6) return vec ? launch_unsort<T, G, uint4, 8, 1>(p, stream) : launch_unsort<T, G, T, 8, 2>(p, stream);
+    if (p.k >= 3) return vec ? launch_unsort<T, G, uint4, 4, 2>(p, stream) : launch_unsort<T, G, T, 4, 4>(p, stream);
+    return vec ? launch_unsort<T, G, uint4, 2, 4>(p, stream) : launch_unsort<T, G, T, 2, 8>(p, stream);
 }
 
 int unsort_run(const UnsortParams& p, bool backward, moe_dtype dtype, moe_dtype gate_dtype, cudaStream_t stream) {
@@ -472,16 +518,11 @@ int unsort_run(const UnsortParams& p, bool backward, moe_dtype dtype, moe_dtype 
                           (uintptr_t)(p.ldbase * es) | (uintptr_t)(p.lddy * es);
     const bool vec = (all & 15) == 0;
     const bool gb = gate_dtype == MOE_BF16;
-    if (dtype == MOE_BF16) {
-        if (vec) return gb ? launch_unsort<__nv_bfloat16, __nv_bfloat16, 8>(p, backward, stream)
-                           : launch_unsort<__nv_bfloat16, float, 8>(p, backward, stream);
-        return gb ? launch_unsort<__nv_bfloat16, __nv_bfloat16, 1>(p, backward, stream)
-                  : launch_unsort<__nv_bfloat16, float, 1>(p, backward, stream);
-    }
-    if (vec) return gb ? launch_unsort<float, __nv_bfloat16, 4>(p, backward, stream)
-                       : launch_unsort<float, float, 4>(p, backward, stream);
-    return gb ? launch_unsort<float, __nv_bfloat16, 1>(p, backward, stream)
-              : launch_unsort<float, float, 1>(p, backward, stream);
+    if (dtype == MOE_BF16)
+        return gb ? launch_back<__nv_bfloat16, __nv_bfloat16>(p, backward, vec, stream)
+                  : launch_back<__nv_bfloat16, float>(p, backward, vec, stream);
+    return gb ? launch_back<float, __nv_bfloat16>(p, backward, vec, stream)
+              : launch_back<float, float>(p, backward, vec, stream);
 }
 
 }  // namespace
