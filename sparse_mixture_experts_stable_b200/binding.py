@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -753,14 +754,19 @@ def _launch(dev: torch.device, stream):
     return _launching(dev, stream)
 
 
+def _ptr(t: Optional[torch.Tensor]):
+    """The address as a plain int: the argtypes convert it, at a third of ``_p``'s cost."""
+    return None if t is None else t.data_ptr()
+
+
 def _take(name: str, t: torch.Tensor, dev: torch.device, dtype=None, shape=None, contiguous: bool = False):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor on a CUDA device")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -770,13 +776,14 @@ def _take(name: str, t: torch.Tensor, dev: torch.device, dtype=None, shape=None,
 def _ld(name: str, t: torch.Tensor, unit: int = 1) -> int:
     """Row stride of a 2-D tensor with unit column stride; a single row's is rounded up to ``unit``."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows <= 1:
         return -(-max(cols, 1) // unit) * unit
-    if t.stride(0) < cols:
+    if ld < cols:
         raise ValueError(f"{name} has overlapping rows")
-    return t.stride(0)
+    return ld
 
 
 def _status(dev_status, dev):
@@ -784,7 +791,7 @@ def _status(dev_status, dev):
         _take("dev_status", dev_status, dev, torch.int32, contiguous=True)
         if dev_status.numel() < 1:
             raise ValueError("dev_status is empty")
-    return _p(dev_status)
+    return _ptr(dev_status)
 
 
 def _scratch(nbytes: int, dev, ws):
@@ -811,7 +818,7 @@ def _out(o: dict, name: str, shape, dtype, dev, fresh: list):
     """o[name] if given (checked), else a new tensor."""
     t = o.get(name)
     if t is None:
-        t = o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        t = o[name] = torch.empty(*shape, dtype=dtype, device=dev)
         fresh.append(t)
     else:
         _take(name, t, dev, dtype, shape, contiguous=True)
@@ -820,7 +827,8 @@ def _out(o: dict, name: str, shape, dtype, dev, fresh: list):
 
 def _padded(rows_shape, K: int, dev) -> torch.Tensor:
     """int8 (*rows_shape, K) whose rows start on multiples of 16 bytes."""
-    return torch.empty(*rows_shape, -(-K // 16) * 16, dtype=torch.int8, device=dev)[..., :K]
+    q = torch.empty(*rows_shape, -(-K // 16) * 16, dtype=torch.int8, device=dev)
+    return q if K % 16 == 0 else q[..., :K]
 
 
 def moe_sort_workspace_size(T: int, k: int, E: int) -> int:
@@ -870,8 +878,8 @@ def moe_sort(selected: torch.Tensor, E: int, x: Optional[torch.Tensor] = None, o
                 _take("xs", xs, dev, x.dtype, (T * k, D))
             ldxs = _ld("xs", xs)
         ws = _scratch(moe_sort_workspace_size(T, k, E), dev, workspace)
-        rc = lib().moe_sort(_p(selected), T, k, E, _p(x), dt, D, ldx, _p(offsets), _p(row), _p(source), _p(xs), ldxs,
-                            _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        rc = lib().moe_sort(_ptr(selected), T, k, E, _ptr(x), dt, D, ldx, _ptr(offsets), _ptr(row), _ptr(source), _ptr(xs), ldxs,
+                            _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
         _check("moe_sort", rc)
         _keep(caller, *fresh)
     return o
@@ -901,8 +909,8 @@ def moe_sort_i8(selected: torch.Tensor, E: int, x: torch.Tensor, out: Optional[d
         else:
             _take("xq", xq, dev, torch.int8, (T * k, D))
         ws = _scratch(moe_sort_workspace_size(T, k, E), dev, workspace)
-        rc = lib().moe_sort_i8(_p(selected), T, k, E, _p(x), dt, D, ldx, _p(offsets), _p(row), _p(source), _p(xq),
-                               _ld("xq", xq), _p(xscale), _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        rc = lib().moe_sort_i8(_ptr(selected), T, k, E, _ptr(x), dt, D, ldx, _ptr(offsets), _ptr(row), _ptr(source), _ptr(xq),
+                               _ld("xq", xq), _ptr(xscale), _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
         _check("moe_sort_i8", rc)
         _keep(caller, *fresh)
     return o
@@ -912,7 +920,7 @@ def _gates(gates, dev, T, k):
     if gates is None:
         return None, MOE_F32
     _take("gates", gates, dev, shape=(T, k), contiguous=True)
-    return _p(gates), _dt(gates)
+    return _ptr(gates), _dt(gates)
 
 
 def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor] = None,
@@ -940,7 +948,7 @@ def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor
             _keep(caller, y)
         else:
             _take("y", y, dev, ys.dtype, (T, N))
-        rc = lib().moe_unsort(_p(ys), _ld("ys", ys), R, _p(row), g, gdt, T, k, N, _p(base), ldb, _p(y), _ld("y", y), dt,
+        rc = lib().moe_unsort(_ptr(ys), _ld("ys", ys), R, _ptr(row), g, gdt, T, k, N, _ptr(base), ldb, _ptr(y), _ld("y", y), dt,
                               _status(dev_status, dev), raw)
         _check("moe_unsort", rc)
     return y
@@ -988,8 +996,8 @@ def moe_unsort_backward(dy: torch.Tensor, ys: Optional[torch.Tensor], row: torch
             fresh.append(dgates)
         else:
             _take("dgates", dgates, dev, torch.float32, (T, k), contiguous=True)
-        rc = lib().moe_unsort_backward(_p(dy), _ld("dy", dy), _p(ys), 0 if ys is None else _ld("ys", ys), rows, _p(row), g,
-                                       gdt, T, k, N, _p(dys), 0 if dys is None else _ld("dys", dys), _p(dgates), dt,
+        rc = lib().moe_unsort_backward(_ptr(dy), _ld("dy", dy), _ptr(ys), 0 if ys is None else _ld("ys", ys), rows, _ptr(row), g,
+                                       gdt, T, k, N, _ptr(dys), 0 if dys is None else _ld("dys", dys), _ptr(dgates), dt,
                                        _status(dev_status, dev), raw)
         _check("moe_unsort_backward", rc)
         _keep(caller, *fresh)
@@ -1008,9 +1016,9 @@ def moe_quantize_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Op
         raise ValueError("x must be (..., K)")
     if x.dim() > 2 and not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    lead, K, dt = tuple(x.shape[:-1]), x.shape[-1], _dt(x)
-    x2 = x if x.dim() == 2 else x.view(-1, K)
-    M = x2.shape[0]
+    *lead, K = x.shape
+    dt = _dt(x)
+    M, ldx = (lead[0], _ld("x", x)) if len(lead) == 1 else (math.prod(lead), max(K, 1))
     with _launch(dev, stream) as (raw, caller):
         fresh = []
         if q is None:
@@ -1019,12 +1027,12 @@ def moe_quantize_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Op
         else:
             _take("q", q, dev, torch.int8, x.shape)
         if scale is None:
-            scale = torch.empty(lead, dtype=torch.float32, device=dev)
+            scale = torch.empty(*lead, dtype=torch.float32, device=dev)
             fresh.append(scale)
         else:
-            _take("scale", scale, dev, torch.float32, lead, contiguous=True)
+            _take("scale", scale, dev, torch.float32, tuple(lead), contiguous=True)
         ldq = _ld3("q", q, 1)
-        rc = lib().moe_quantize_i8(_p(x), dt, M, K, _ld("x", x2), _p(q), ldq, _p(scale), _status(dev_status, dev), raw)
+        rc = lib().moe_quantize_i8(_ptr(x), dt, M, K, ldx, _ptr(q), ldq, _ptr(scale), _status(dev_status, dev), raw)
         _check("moe_quantize_i8", rc)
         _keep(caller, *fresh)
     return q, scale
@@ -1057,7 +1065,7 @@ def _ld3(name: str, t: torch.Tensor, unit: int) -> int:
 def _weight_i8(name, w, scale, dev, G, N, K):
     """Checks an 8-bit weight (G, N, K) or, for G = 1, (N, K) with its scales; returns the row stride."""
     _take(name, w, dev, torch.int8)
-    if tuple(w.shape) not in ((G, N, K), (N, K) if G == 1 else (G, N, K)):
+    if w.shape != (G, N, K) and (G != 1 or w.shape != (N, K)):
         raise ValueError(f"{name} must be ({G}, {N}, {K}), got {tuple(w.shape)}")
     _take(f"{name}'s scale", scale, dev, torch.float32, contiguous=True)
     if scale.numel() != G * N:
@@ -1084,7 +1092,7 @@ def _bias_i8(name, b, dev, G, N):
         _take(name, b, dev, torch.float32, contiguous=True)
         if b.numel() != G * N:
             raise ValueError(f"{name} must hold {G * N} values")
-    return _p(b)
+    return _ptr(b)
 
 
 def _out_dt(out, out_dtype):
@@ -1120,8 +1128,8 @@ def moe_matmul_i8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wsca
         else:
             _take("out", out, dev, dtype, (M, N))
         ws = _scratch(int(lib().moe_matmul_i8_workspace_size(M, G, N, K)), dev, workspace)
-        rc = lib().moe_matmul_i8(_p(xq), _p(xscale), M, _ld("xq", xq, 16), _p(offsets), _p(wq), _p(wscale), ldw, b, G, N, K,
-                                 _p(out), _ld("out", out), dt, _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        rc = lib().moe_matmul_i8(_ptr(xq), _ptr(xscale), M, _ld("xq", xq, 16), _ptr(offsets), _ptr(wq), _ptr(wscale), ldw, b, G, N, K,
+                                 _ptr(out), _ld("out", out), dt, _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
         _check("moe_matmul_i8", rc)
     return out
 
@@ -1178,9 +1186,9 @@ def moe_expert_ffn_i8(kind: str, xq: torch.Tensor, xscale: torch.Tensor, offsets
         else:
             _take("ys", ys, dev, dtype, (M, Dout))
         ws = _scratch(moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout), dev, workspace)
-        rc = lib().moe_expert_ffn_i8(FFN[kind], _p(xq), _p(xscale), M, _ld("xq", xq, 16), _p(offsets), G, D, F, Dout,
-                                     _p(w1), _p(s1), ld1, pb1, _p(w2), _p(s2), ld2, pb2, _p(w3), _p(s3), _p(ys),
-                                     _ld("ys", ys), dt, _status(dev_status, dev), _p(ws), _nbytes(ws), raw)
+        rc = lib().moe_expert_ffn_i8(FFN[kind], _ptr(xq), _ptr(xscale), M, _ld("xq", xq, 16), _ptr(offsets), G, D, F, Dout,
+                                     _ptr(w1), _ptr(s1), ld1, pb1, _ptr(w2), _ptr(s2), ld2, pb2, _ptr(w3), _ptr(s3), _ptr(ys),
+                                     _ld("ys", ys), dt, _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
         _check("moe_expert_ffn_i8", rc)
     return ys
 

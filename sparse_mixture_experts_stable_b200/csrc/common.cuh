@@ -94,4 +94,32 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
     return m;
 }
 
+// ---------------------------------------------------------------------------
+// programmatic dependent launch: the next kernel of the stream is set up, and its
+// blocks wait in pdl_wait, while the one before it finishes
+// ---------------------------------------------------------------------------
+// Returns once the kernels before this one in the stream are complete and their writes
+// visible.  Comes before any access to global memory.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the stream's next kernel be set up once every block has come here.
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel that begins with pdl_wait.
+template <typename... P, typename... A>
+inline int launch_pdl(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess) return MOE_OK;
+    (void)cudaGetLastError();  // reported here; later calls do not find it again
+    return MOE_ERR_CUDA;
+}
+
 }  // namespace moe

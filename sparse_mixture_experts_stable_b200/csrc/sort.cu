@@ -4,10 +4,15 @@
 // Assignments i = t k + j are ordered by (expert, i): row = offsets[e] + #{earlier
 // assignments to e}.  The order is a counting sort.  Up to kSmallCount assignments one
 // launch does everything: every block counts all the keys itself, so no block waits
-// for another.  Above, hist_kernel counts the keys of each super-block, base_kernel
-// turns the counts into first rows, and every block of the row kernel adds the keys of
-// its super-block that come before its own tokens.  Integer counts do not depend on
-// the order of the shared-memory atomics that make them, so the rows are unique.
+// for another, and copies (or quantises) its tokens' rows.  Above, hist_kernel counts the
+// keys of each super-block, rank_kernel adds those of all the super-blocks (at most
+// kMaxCounts counts, so each block does it for itself) and ranks the keys of its own by
+// warp, and a last kernel writes the packed rows:
+// one warp per assignment, so that a block's warps read the same token's row and write
+// different ones (short blocks: the same rows written by 512 long-lived blocks took 117 us
+// for T = 16384, k = 8, D = 2048 bf16).  Rows in 8 bits are quantised once per token, into
+// shared memory.  Integer counts do not depend on the order of the shared-memory atomics
+// that make them, so the rows are unique.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,9 +28,14 @@ constexpr int kMaxK = 64;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int64_t kSmallCount = 4096;   // assignments that one launch handles by itself
-constexpr int64_t kSuperCount = 4096;   // assignments per super-block (more when there are over kMaxSuper of them)
-constexpr int64_t kMaxSuper = 256;
+// Assignments per super-block: a 64th of all, from 1024 to 4096, or more where the counts would pass kMaxCounts.
+// Larger ones make rank_kernel's chain longer, smaller ones its reads of all the counts: the order of n = 131072,
+// E = 256 takes 19.2 us with 1024, 10.9 with 2048 and 13.5 with 4096; n = 16382, E = 64 6.3, 7.7 and 11.9 us.
+constexpr int64_t kMinSuper = 1024, kMaxSuper = 4096;
+constexpr int64_t kMaxCounts = 65536;  // super-blocks * E that every block of rank_kernel reads
 constexpr int kHistThreads = 512;
+constexpr int kRankThreads = 512;
+constexpr int kRankWarps = kRankThreads / 32;
 
 // What the row kernel does with each token's row of x.
 enum RowOp : int { ROW_NONE = 0, ROW_COPY = 1, ROW_I8 = 2 };
@@ -35,9 +45,10 @@ struct SortParams {
     int64_t T;
     int k, E;
     int64_t n;            // T * k
-    int64_t super;        // assignments per super-block (a multiple of k), 0 in the one-launch form
-    int64_t block_tokens; // tokens per block of the row kernel
-    const int32_t* base;  // (super-blocks, E) first rows inside the expert, from base_kernel
+    int64_t super;        // assignments per super-block
+    int64_t block_tokens; // tokens per block of the one-launch form
+    const int32_t* hist;  // (super-blocks, E) counts, from hist_kernel
+    int n_super;
     int32_t* offsets;
     int32_t* row;
     int32_t* source;
@@ -46,7 +57,7 @@ struct SortParams {
     void* xs;
     int64_t ldxs;
     float* xscale;
-    bool vec;             // ROW_I8: x rows start on 16 bytes, xs rows on 8
+    bool vecx, vecq;      // ROW_I8: x rows start on 16 bytes, xs rows on 8
     int32_t* status;
 };
 
@@ -57,180 +68,281 @@ __device__ __forceinline__ int key_of(int64_t e, int E, int32_t* status) {
     return -1;
 }
 
-__global__ void __launch_bounds__(kHistThreads)
-    hist_kernel(const int64_t* __restrict__ selected, int64_t n, int64_t super, int E, int32_t* __restrict__ hist,
-                int32_t* status) {
+// hist[super-block][e]: its keys of expert e
+__global__ void __launch_bounds__(kHistThreads) hist_kernel(const SortParams p, int32_t* __restrict__ hist) {
     extern __shared__ int s_cnt[];
-    for (int e = threadIdx.x; e < E; e += kHistThreads) s_cnt[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += kHistThreads) s_cnt[e] = 0;
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * super;
-    const int64_t last = first + super < n ? first + super : n;
-#pragma unroll 4
+    const int64_t first = (int64_t)blockIdx.x * p.super;
+    const int64_t last = first + p.super < p.n ? first + p.super : p.n;
+    pdl_wait();
+    pdl_next();
+#pragma unroll 8
     for (int64_t i = first + threadIdx.x; i < last; i += kHistThreads) {
-        const int key = key_of(selected[i], E, status);
+        const int key = key_of(p.selected[i], p.E, p.status);
         if (key >= 0) atomicAdd(&s_cnt[key], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kHistThreads) hist[(int64_t)blockIdx.x * E + e] = s_cnt[e];
+    for (int e = threadIdx.x; e < p.E; e += kHistThreads) hist[(int64_t)blockIdx.x * p.E + e] = s_cnt[e];
 }
 
-constexpr int kBaseThreads = 1024;
-constexpr int kBaseBatch = 16;
+// rows of the chunk's 32 assignments: next[key] + the lanes before with the same key; next moves on
+__device__ __forceinline__ int rank_chunk(int key, int* next, int lane) {
+    const uint32_t match = __match_any_sync(0xffffffffu, key);
+    int r = -1;
+    if (key >= 0) r = next[key] + __popc(match & lanemask_lt());
+    __syncwarp();
+    if (key >= 0 && __ffs(match) - 1 == lane) next[key] += __popc(match);
+    __syncwarp();
+    return r;
+}
 
-// hist (n_super, E) -> exclusive sums over the super-blocks in place, and offsets (E + 1).
-__global__ void __launch_bounds__(kBaseThreads)
-    base_kernel(int32_t* hist, int n_super, int E, int32_t* __restrict__ offsets) {
-    __shared__ int s_total[kMaxE + 1];
-    for (int e = threadIdx.x; e < E; e += kBaseThreads) {
-        int run = 0;
-        for (int a0 = 0; a0 < n_super; a0 += kBaseBatch) {
-            int v[kBaseBatch];
-#pragma unroll
-            for (int u = 0; u < kBaseBatch; ++u) v[u] = a0 + u < n_super ? hist[(int64_t)(a0 + u) * E + e] : 0;
-#pragma unroll
-            for (int u = 0; u < kBaseBatch; ++u)
-                if (a0 + u < n_super) {
-                    hist[(int64_t)(a0 + u) * E + e] = run;
-                    run += v[u];
-                }
+__device__ __forceinline__ void put_rank(const SortParams& p, int64_t i, int r, int total) {
+    p.row[i] = r;
+    if (r >= 0) p.source[r] = (int32_t)i;
+    if (i >= total) p.source[i] = -1;  // behind the last row
+}
+
+// One block per super-block: its warps take consecutive pieces, count them, and rank them from where the warps before
+// end.  Shared memory: counts (warps, E).
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const SortParams p, int warps) {
+    extern __shared__ int s_cnt[];
+    __shared__ int s_total[kMaxE + 1];    // sums over all super-blocks, then over the experts before
+    __shared__ int s_before[kMaxE];       // sums over the super-blocks before this one
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < warps * p.E; i += kRankThreads) s_cnt[i] = 0;
+    for (int e = threadIdx.x; e < p.E; e += kRankThreads) s_total[e] = s_before[e] = 0;
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * p.super;
+    const int64_t last = first + p.super < p.n ? first + p.super : p.n;
+    const int64_t piece = (p.super + warps * 32 - 1) / (warps * 32) * 32;
+    const int64_t w0 = first + warp * piece, w1 = w0 + piece < last ? w0 + piece : last;
+    int* cnt = s_cnt + warp * p.E;
+    pdl_wait();
+    pdl_next();
+    if (warp < warps) {
+#pragma unroll 2
+        for (int64_t i = w0 + lane; i < w1; i += 32) {
+            const int key = key_of(p.selected[i], p.E, nullptr);
+            if (key >= 0) atomicAdd(&cnt[key], 1);
         }
-        s_total[e] = run;
+    }
+    // the threads of an expert share the super-blocks
+    const int segs = p.E < kRankThreads ? kRankThreads / p.E : 1;
+    const int seg = p.E < kRankThreads ? threadIdx.x / p.E : 0;
+    for (int e = threadIdx.x - seg * p.E; seg < segs && e < p.E; e += kRankThreads) {
+        int total = 0, before = 0;
+#pragma unroll 8
+        for (int i = seg; i < p.n_super; i += segs) {
+            // from the own super-block on, so that the blocks do not all ask for the same counts at once
+            const int a = i + blockIdx.x < p.n_super ? i + blockIdx.x : i + blockIdx.x - p.n_super;
+            const int c = p.hist[(int64_t)a * p.E + e];
+            total += c;
+            before += a < blockIdx.x ? c : 0;
+        }
+        atomicAdd(&s_total[e], total);
+        atomicAdd(&s_before[e], before);
     }
     __syncthreads();
-    block_scan<kBaseThreads>(s_total, E);
-    for (int e = threadIdx.x; e <= E; e += kBaseThreads) offsets[e] = s_total[e];
+    block_scan<kRankThreads>(s_total, p.E);
+    for (int e = threadIdx.x; e < p.E; e += kRankThreads) {
+        int run = s_total[e] + s_before[e];
+        for (int w = 0; w < warps; ++w) {
+            const int c = s_cnt[w * p.E + e];
+            s_cnt[w * p.E + e] = run;
+            run += c;
+        }
+    }
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= p.E; e += kRankThreads) p.offsets[e] = s_total[e];
+    __syncthreads();
+    if (warp >= warps) return;
+    const int total = s_total[p.E];
+#pragma unroll 2
+    for (int64_t c = w0; c < w1; c += 32) {
+        const int64_t i = c + lane;
+        const int r = rank_chunk(i < w1 ? key_of(p.selected[i], p.E, nullptr) : -1, cnt, lane);
+        if (i < w1) put_rank(p, i, r, total);
+    }
 }
 
-// One warp copies a row to the rows dst[0..k) of the packed matrix (-1: none).
+// The TEAM threads from 0 on copy a row to the rows dst[0..k) of the packed matrix (-1: none).
 // V: the widest vector that every row start and the row length allow.
-template <typename V>
-__device__ __forceinline__ void copy_row(const SortParams& p, int64_t t, const int* rows, int lane) {
+template <int TEAM, typename V>
+__device__ __forceinline__ void copy_row(const SortParams& p, int64_t t, const int* rows, int tid) {
     constexpr int kBatch = 8;
     const int64_t nv = p.D, ldx = p.ldx, lds = p.ldxs;  // in units of V
     const V* src = static_cast<const V*>(p.x) + t * ldx;
     V* dst = static_cast<V*>(p.xs);
-    for (int64_t v0 = lane; v0 < nv; v0 += 32 * kBatch) {
+    for (int64_t v0 = tid; v0 < nv; v0 += TEAM * kBatch) {
         V r[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            if (v0 + 32 * u < nv) r[u] = src[v0 + 32 * u];
+            if (v0 + TEAM * u < nv) r[u] = src[v0 + TEAM * u];
         for (int j = 0; j < p.k; ++j) {
             const int rw = rows[j];
             if (rw < 0) continue;
             V* d = dst + (int64_t)rw * lds;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
-                if (v0 + 32 * u < nv) d[v0 + 32 * u] = r[u];
+                if (v0 + TEAM * u < nv) d[v0 + TEAM * u] = r[u];
         }
     }
 }
 
-// Shared memory: s_cnt[E + 1] (next row of each expert), s_row[block_tokens * k]; one-launch form: s_off[E + 1] too.
-template <int OP, typename V>
-__global__ void __launch_bounds__(kThreads) row_kernel(const SortParams p) {
+// The one-launch form: the order, and the rows (OP).  WARPS: warps per token, one or the whole block.
+// Shared memory: s_cnt[E + 1] (next row of each expert), s_off[E + 1], s_row[block_tokens * k].
+template <int OP, int WARPS, typename V>
+__global__ void __launch_bounds__(kThreads, OP == ROW_I8 ? 3 : 4) small_kernel(const SortParams p) {
     extern __shared__ int s_dyn[];
+    __shared__ uint32_t s_max[kWarps];
     int* s_cnt = s_dyn;
-    int* s_row = s_cnt + p.E + 1;
+    int* s_off = s_cnt + p.E + 1;
+    int* s_row = s_off + p.E + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * p.block_tokens;
     const int ntok = (int)(p.T - t0 < p.block_tokens ? p.T - t0 : p.block_tokens);
     const int64_t first = t0 * p.k;  // this block's assignments: [first, first + n_own)
     const int n_own = ntok * p.k;
-
-    int total;
-    if (p.super == 0) {
-        int* s_off = s_row + p.block_tokens * p.k;
-        for (int e = threadIdx.x; e < p.E; e += kThreads) s_cnt[e] = s_off[e] = 0;
-        __syncthreads();
-        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
-            const int key = key_of(p.selected[i], p.E, p.status);
-            if (key >= 0) {
-                atomicAdd(&s_off[key], 1);
-                if (i < first) atomicAdd(&s_cnt[key], 1);
-            }
+    for (int e = threadIdx.x; e < p.E; e += kThreads) s_cnt[e] = s_off[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_next();
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
+        const int key = key_of(p.selected[i], p.E, p.status);
+        if (key >= 0) {
+            atomicAdd(&s_off[key], 1);
+            if (i < first) atomicAdd(&s_cnt[key], 1);
         }
-        __syncthreads();
-        block_scan<kThreads>(s_off, p.E);
-        for (int e = threadIdx.x; e < p.E; e += kThreads) s_cnt[e] += s_off[e];
-        if (blockIdx.x == 0)
-            for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = s_off[e];
-        total = s_off[p.E];
-    } else {
-        const int64_t a = first / p.super;
-        for (int e = threadIdx.x; e < p.E; e += kThreads) s_cnt[e] = p.base[a * p.E + e] + p.offsets[e];
-        __syncthreads();
-        for (int64_t i = a * p.super + threadIdx.x; i < first; i += kThreads) {
-            const int key = key_of(p.selected[i], p.E, nullptr);
-            if (key >= 0) atomicAdd(&s_cnt[key], 1);
-        }
-        total = p.offsets[p.E];
     }
+    __syncthreads();
+    block_scan<kThreads>(s_off, p.E);
+    for (int e = threadIdx.x; e < p.E; e += kThreads) s_cnt[e] += s_off[e];
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = s_off[e];
     __syncthreads();
 
     // ranks of the own assignments, 32 at a time in order
     if (warp == 0) {
+        const int total = s_off[p.E];
         for (int c = 0; c < n_own; c += 32) {
             const int li = c + lane;
-            const int key = li < n_own ? key_of(p.selected[first + li], p.E, nullptr) : -1;
-            const uint32_t match = __match_any_sync(0xffffffffu, key);
-            int r = -1;
-            if (key >= 0) r = s_cnt[key] + __popc(match & lanemask_lt());
-            __syncwarp();
-            if (key >= 0 && __ffs(match) - 1 == lane) s_cnt[key] += __popc(match);
-            __syncwarp();
+            const int r = rank_chunk(li < n_own ? key_of(p.selected[first + li], p.E, nullptr) : -1, s_cnt, lane);
             if (li < n_own) {
                 s_row[li] = r;
-                p.row[first + li] = r;
-                if (r >= 0) p.source[r] = (int32_t)(first + li);
-                if (first + li >= total) p.source[first + li] = -1;  // behind the last row
+                put_rank(p, first + li, r, total);
             }
         }
     }
     if (OP == ROW_NONE) return;
     __syncthreads();
-    for (int t = warp; t < ntok; t += kWarps) {
+    const int tid = WARPS == 1 ? lane : threadIdx.x;
+    for (int t = WARPS == 1 ? warp : 0; t < ntok; t += kWarps / WARPS) {
         const int* rows = s_row + t * p.k;
-        if (OP == ROW_COPY) copy_row<V>(p, t0 + t, rows, lane);
-        if (OP == ROW_I8) {
+        if constexpr (OP == ROW_COPY) copy_row<32 * WARPS, V>(p, t0 + t, rows, tid);
+        if constexpr (OP == ROW_I8) {
             int8_t* q = static_cast<int8_t*>(p.xs);
-            const float scale = quantize_row_warp(static_cast<const V*>(p.x) + (t0 + t) * p.ldx, p.D, rows, p.k, q,
-                                                  p.ldxs, p.vec, p.status);
-            for (int j = lane; j < p.k; j += 32)
+            const float scale = quantize_row<WARPS>(static_cast<const V*>(p.x) + (t0 + t) * p.ldx, p.D, rows, p.k, q,
+                                                    p.ldxs, p.vecx, p.vecq, s_max, p.status);
+            for (int j = tid; j < p.k; j += 32 * WARPS)
                 if (rows[j] >= 0) p.xscale[rows[j]] = scale;
         }
     }
 }
 
-// super-block and row-block sizes for T tokens of k assignments
+// xs[row[t, j]] = x[t] (both in units of V), one assignment per 2^shift lanes.
+template <typename V>
+__global__ void __launch_bounds__(kThreads) scatter_kernel(const SortParams p, int shift) {
+    constexpr int kBatch = 8;
+    const int lane = threadIdx.x & 31, team = 1 << shift;
+    const int64_t i = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 >> shift) + (lane >> shift);
+    pdl_wait();
+    pdl_next();
+    if (i >= p.n) return;
+    const int r = p.row[i];
+    if (r < 0) return;
+    const V* src = static_cast<const V*>(p.x) + (i / p.k) * p.ldx;
+    V* dst = static_cast<V*>(p.xs) + r * p.ldxs;
+    for (int64_t v0 = lane & (team - 1); v0 < p.D; v0 += team * kBatch) {
+        V v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (v0 + team * u < p.D) v[u] = src[v0 + team * u];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (v0 + team * u < p.D) __stcs(dst + v0 + team * u, v[u]);
+    }
+}
+
+constexpr int kI8Threads = 128;
+constexpr int kI8Seg = 8192;  // values of a row in shared memory at a time
+
+// The same in 8 bits: a block per token quantises its row into shared memory, from where each warp writes every fourth
+// of the token's rows.  Where the rows do not lie on 16 bytes, or are no longer than a warp's eight steps, a warp per
+// token writes them as it goes.
+template <typename T, bool SHARED>
+__global__ void __launch_bounds__(kI8Threads) scatter_i8_kernel(const SortParams p) {
+    __shared__ uint32_t s_max[kI8Threads / 32];
+    __shared__ int s_row[SHARED ? 1 : kI8Threads / 32][kMaxK];
+    extern __shared__ uint4 s_q[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = SHARED ? blockIdx.x : (int64_t)blockIdx.x * (kI8Threads / 32) + warp;
+    pdl_wait();
+    pdl_next();
+    if (t >= p.T) return;
+    int* rows = s_row[SHARED ? 0 : warp];
+    for (int j = SHARED ? threadIdx.x : lane; j < p.k; j += SHARED ? kI8Threads : 32) rows[j] = p.row[t * p.k + j];
+    const T* src = static_cast<const T*>(p.x) + t * p.ldx;
+    int8_t* q = static_cast<int8_t*>(p.xs);
+    float scale;
+    if constexpr (SHARED) {
+        const RowQuant r = row_quant(row_max<kI8Threads / 32>(src, p.D, p.vecx, s_max), p.status, threadIdx.x == 0);
+        scale = r.scale;
+        for (int64_t s0 = 0; s0 < p.D; s0 += kI8Seg) {
+            const int len = (int)(p.D - s0 < kI8Seg ? p.D - s0 : kI8Seg);
+            if (s0 > 0) __syncthreads();  // the segment before has been written
+            for (int c = threadIdx.x * kChunk<T>; c < len; c += kI8Threads * kChunk<T>) {
+                Raw<T> x;
+                x.load(src + s0 + c, len - c, p.vecx);
+                uint32_t o[kChunk<T> / 4];
+                quantize_chunk(x, r, o);
+                store_chunk(reinterpret_cast<int8_t*>(s_q) + c, o, kChunk<T>, true);
+            }
+            __syncthreads();
+            for (int j = warp; j < p.k; j += kI8Threads / 32) {
+                if (rows[j] < 0) continue;
+                int8_t* dst = q + (int64_t)rows[j] * p.ldxs + s0;
+                for (int c = lane; c < len / 16; c += 32) __stcs(reinterpret_cast<uint4*>(dst) + c, s_q[c]);
+                for (int c = len / 16 * 16 + lane; c < len; c += 32) dst[c] = reinterpret_cast<const int8_t*>(s_q)[c];
+            }
+        }
+    } else {
+        __syncwarp();
+        scale = quantize_row<1>(src, p.D, rows, p.k, q, p.ldxs, p.vecx, p.vecq, s_max, p.status);
+    }
+    for (int j = SHARED ? threadIdx.x : lane; j < p.k; j += SHARED ? kI8Threads : 32)
+        if (rows[j] >= 0) p.xscale[rows[j]] = scale;
+}
+
+// super-blocks, or the one-launch form's blocks, for T tokens of k assignments
 struct SortPlan {
     bool small;
     int64_t super, n_super, block_tokens;
 };
 
-SortPlan sort_plan(int64_t T, int32_t k) {
+SortPlan sort_plan(int64_t T, int32_t k, int32_t E) {
     SortPlan s{};
     const int64_t n = T * k;
     const int64_t sms = device_sm_count();
     s.small = n <= kSmallCount;
-    if (s.small) {
-        s.block_tokens = (T + 2 * sms - 1) / (2 * sms);
-    } else {
-        int64_t bt = 32;                          // T = 16384: 512 blocks
-        while (bt > 1 && bt * k > 1024) bt >>= 1; // the rows of a block stay in shared memory
-        s.block_tokens = bt;
-        int64_t super = n / kMaxSuper > kSuperCount ? n / kMaxSuper : kSuperCount;
-        const int64_t unit = bt * k;              // whole blocks per super-block
-        s.super = (super + unit - 1) / unit * unit;
-        s.n_super = (n + s.super - 1) / s.super;
-    }
+    s.block_tokens = (T + 2 * sms - 1) / (2 * sms);
     if (s.block_tokens < 1) s.block_tokens = 1;
+    s.super = n / 64 < kMinSuper ? kMinSuper : n / 64 > kMaxSuper ? kMaxSuper : n / 64;
+    const int64_t most = kMaxCounts / E;
+    if (n > most * s.super) s.super = (n + most - 1) / most;
+    s.n_super = (n + s.super - 1) / s.super;
     return s;
-}
-
-template <int OP, typename V>
-int launch_rows(const SortParams& p, int64_t blocks, size_t smem, cudaStream_t stream) {
-    row_kernel<OP, V><<<(unsigned)blocks, kThreads, smem, stream>>>(p);
-    return launch_status();
 }
 
 int sort_check(const int64_t* selected, int64_t T, int32_t k, int32_t E, const int32_t* offsets, const int32_t* row,
@@ -243,8 +355,58 @@ int sort_check(const int64_t* selected, int64_t T, int32_t k, int32_t E, const i
 }
 
 size_t sort_workspace(int64_t T, int32_t k, int32_t E) {
-    const SortPlan s = sort_plan(T, k);
+    const SortPlan s = sort_plan(T, k, E);
     return s.small ? 0 : align_up((size_t)s.n_super * E * sizeof(int32_t), 256);
+}
+
+// the widest vector that the rows' starts, strides and length allow: their units of 1 << result bytes
+int row_vector(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t D, size_t es) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | (uintptr_t)(D * es) |
+                          (uintptr_t)(lda * es) | (uintptr_t)(ldb * es);
+    return (all & 15) == 0 ? 4 : (all & 3) == 0 ? 2 : (all & 1) == 0 ? 1 : 0;
+}
+
+int launch_scatter(SortParams p, size_t es, cudaStream_t stream) {
+    const int bits = row_vector(p.x, p.ldx, p.xs, p.ldxs, p.D, es);
+    p.D = p.D * es >> bits, p.ldx = p.ldx * es >> bits, p.ldxs = p.ldxs * es >> bits;
+    int shift = 0;
+    while (shift < 5 && (1 << shift) < p.D) ++shift;
+    const int64_t per_block = kWarps * (32 >> shift);
+    const int64_t grid = (p.n + per_block - 1) / per_block;
+    if (bits == 4) return launch_pdl(scatter_kernel<uint4>, grid, kThreads, 0, stream, p, shift);
+    if (bits == 2) return launch_pdl(scatter_kernel<uint32_t>, grid, kThreads, 0, stream, p, shift);
+    return launch_pdl(scatter_kernel<uint16_t>, grid, kThreads, 0, stream, p, shift);
+}
+
+template <typename T>
+int launch_scatter_i8(const SortParams& p, cudaStream_t stream) {
+    constexpr int kPer = kI8Threads / 32;
+    if (p.D <= 32 * kChunk<T> * 2 || !aligned16(p.xs) || p.ldxs % 16)
+        return launch_pdl(scatter_i8_kernel<T, false>, (p.T + kPer - 1) / kPer, kI8Threads, 0, stream, p);
+    const size_t smem = align_up((size_t)(p.D < kI8Seg ? p.D : kI8Seg), 16);
+    return launch_pdl(scatter_i8_kernel<T, true>, p.T, kI8Threads, smem, stream, p);
+}
+
+// The order, and the rows by token (op), few blocks: every block counts all the keys.
+int sort_small(SortParams p, int op, moe_dtype dtype, cudaStream_t stream) {
+    const int64_t blocks = (p.T + p.block_tokens - 1) / p.block_tokens;
+    const size_t smem = sizeof(int) * (2 * ((size_t)p.E + 1) + (size_t)p.block_tokens * p.k);
+    const auto go = [&](auto kernel) { return launch_pdl(kernel, blocks, kThreads, smem, stream, p); };
+    const bool share = p.block_tokens < kWarps;  // few tokens per block: its warps share each row
+    if (op == ROW_NONE) return go(small_kernel<ROW_NONE, 1, float>);
+    if (op == ROW_I8) {
+        if (dtype == MOE_BF16)
+            return share ? go(small_kernel<ROW_I8, kWarps, __nv_bfloat16>)
+                         : go(small_kernel<ROW_I8, 1, __nv_bfloat16>);
+        return share ? go(small_kernel<ROW_I8, kWarps, float>) : go(small_kernel<ROW_I8, 1, float>);
+    }
+    const size_t es = dtype_size(dtype);
+    const int bits = row_vector(p.x, p.ldx, p.xs, p.ldxs, p.D, es);
+    p.D = p.D * es >> bits, p.ldx = p.ldx * es >> bits, p.ldxs = p.ldxs * es >> bits;
+    if (bits == 4) return share ? go(small_kernel<ROW_COPY, kWarps, uint4>) : go(small_kernel<ROW_COPY, 1, uint4>);
+    if (bits == 2)
+        return share ? go(small_kernel<ROW_COPY, kWarps, uint32_t>) : go(small_kernel<ROW_COPY, 1, uint32_t>);
+    return share ? go(small_kernel<ROW_COPY, kWarps, uint16_t>) : go(small_kernel<ROW_COPY, 1, uint16_t>);
 }
 
 // The order, then the rows of x (op).
@@ -253,41 +415,26 @@ int sort_run(SortParams p, int op, moe_dtype dtype, void* workspace, size_t work
         MOE_CUDA_TRY(cudaMemsetAsync(p.offsets, 0, sizeof(int32_t) * ((size_t)p.E + 1), stream));
         return MOE_OK;
     }
-    const SortPlan s = sort_plan(p.T, p.k);
+    const SortPlan s = sort_plan(p.T, p.k, p.E);
     p.n = p.T * p.k;
-    p.super = s.small ? 0 : s.super;
+    p.super = s.super;
     p.block_tokens = s.block_tokens;
-    if (!s.small) {
-        MOE_REQUIRE(workspace && workspace_bytes >= sort_workspace(p.T, p.k, p.E), MOE_ERR_WORKSPACE);
-        int32_t* hist = static_cast<int32_t*>(workspace);
-        p.base = hist;
-        hist_kernel<<<(unsigned)s.n_super, kHistThreads, sizeof(int) * p.E, stream>>>(p.selected, p.n, p.super, p.E,
-                                                                                      hist, p.status);
-        int rc = launch_status();
-        if (rc != MOE_OK) return rc;
-        base_kernel<<<1, kBaseThreads, 0, stream>>>(hist, (int)s.n_super, p.E, p.offsets);
-        rc = launch_status();
-        if (rc != MOE_OK) return rc;
-    }
-    const int64_t blocks = (p.T + s.block_tokens - 1) / s.block_tokens;
-    const size_t smem = sizeof(int) * ((size_t)(s.small ? 2 : 1) * (p.E + 1) + (size_t)s.block_tokens * p.k);
-    if (op == ROW_NONE) return launch_rows<ROW_NONE, float>(p, blocks, smem, stream);
     if (op == ROW_I8) {
-        p.vec = aligned16(p.x) && (p.ldx * dtype_size(dtype)) % 16 == 0 &&
-                (reinterpret_cast<uintptr_t>(p.xs) & 7) == 0 && p.ldxs % 8 == 0;
-        return dtype == MOE_BF16 ? launch_rows<ROW_I8, __nv_bfloat16>(p, blocks, smem, stream)
-                                 : launch_rows<ROW_I8, float>(p, blocks, smem, stream);
+        p.vecx = aligned16(p.x) && (p.ldx * dtype_size(dtype)) % 16 == 0;
+        p.vecq = (reinterpret_cast<uintptr_t>(p.xs) & 7) == 0 && p.ldxs % 8 == 0;
     }
-    const size_t es = dtype_size(dtype);
-    const uintptr_t all = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.xs) |
-                          (uintptr_t)(p.D * es) | (uintptr_t)(p.ldx * es) | (uintptr_t)(p.ldxs * es);
-    const int64_t per = (all & 15) == 0 ? 16 / es : (all & 3) == 0 ? 4 / es : 1;  // elements per vector
-    p.D /= per;
-    p.ldx /= per;
-    p.ldxs /= per;
-    if ((all & 15) == 0) return launch_rows<ROW_COPY, uint4>(p, blocks, smem, stream);
-    if ((all & 3) == 0) return launch_rows<ROW_COPY, uint32_t>(p, blocks, smem, stream);
-    return launch_rows<ROW_COPY, uint16_t>(p, blocks, smem, stream);
+    if (s.small) return sort_small(p, op, dtype, stream);
+
+    MOE_REQUIRE(workspace && workspace_bytes >= sort_workspace(p.T, p.k, p.E), MOE_ERR_WORKSPACE);
+    int32_t* hist = static_cast<int32_t*>(workspace);
+    p.hist = hist, p.n_super = (int)s.n_super;
+    int rc = launch_pdl(hist_kernel, s.n_super, kHistThreads, sizeof(int) * p.E, stream, p, hist);
+    if (rc != MOE_OK) return rc;
+    const int warps = 7168 / p.E < kRankWarps ? 7168 / p.E : kRankWarps;  // as many as 28 KB of counts allow
+    rc = launch_pdl(rank_kernel, s.n_super, kRankThreads, sizeof(int) * p.E * warps, stream, p, warps);
+    if (rc != MOE_OK || op == ROW_NONE) return rc;
+    if (op == ROW_COPY) return launch_scatter(p, dtype_size(dtype), stream);
+    return dtype == MOE_BF16 ? launch_scatter_i8<__nv_bfloat16>(p, stream) : launch_scatter_i8<float>(p, stream);
 }
 
 // ------------------------------- and back -----------------------------------
@@ -392,6 +539,8 @@ __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
     const int64_t t = unit / p.split;
+    pdl_wait();
+    pdl_next();
     if (t >= p.T) return;
     const int n = token_rows<G>(p, t, lane, s_row[warp], s_gate[warp]);
     const T* ys = static_cast<const T*>(p.ys);
@@ -432,6 +581,8 @@ __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const UnsortP
     constexpr int N = Vec<T, V>::kN;
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_next();
     if (unit >= p.T * p.k) return;
     const int64_t t = unit / p.k;
     const int64_t r = p.row[unit];
@@ -488,17 +639,15 @@ int launch_unsort(UnsortParams p, cudaStream_t stream) {
     const int64_t want = (int64_t)device_sm_count() * kFill / p.T;
     p.split = (int)(want < 1 ? 1 : want < groups ? want : groups);
     const int64_t grid = (p.T * p.split + kWarps - 1) / kWarps;
-    unsort_kernel<T, G, V, J, U><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-    return launch_status();
+    return launch_pdl(unsort_kernel<T, G, V, J, U>, grid, kThreads, 0, stream, p);
 }
 
 template <typename T, typename G, typename V, int U>
 int launch_backward(const UnsortParams& p, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((p.T * p.k + kWarps - 1) / kWarps);
-    if (p.y && p.dgates) unsort_backward_kernel<T, G, V, U, true, true><<<grid, kThreads, 0, stream>>>(p);
-    else if (p.y) unsort_backward_kernel<T, G, V, U, true, false><<<grid, kThreads, 0, stream>>>(p);
-    else unsort_backward_kernel<T, G, V, U, false, true><<<grid, kThreads, 0, stream>>>(p);
-    return launch_status();
+    const int64_t grid = (p.T * p.k + kWarps - 1) / kWarps;
+    if (p.y && p.dgates) return launch_pdl(unsort_backward_kernel<T, G, V, U, true, true>, grid, kThreads, 0, stream, p);
+    if (p.y) return launch_pdl(unsort_backward_kernel<T, G, V, U, true, false>, grid, kThreads, 0, stream, p);
+    return launch_pdl(unsort_backward_kernel<T, G, V, U, false, true>, grid, kThreads, 0, stream, p);
 }
 
 // Rows that 16 bytes divide, or single elements (two loads for each of the 16-byte form's).
