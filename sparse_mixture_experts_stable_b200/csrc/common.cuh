@@ -106,20 +106,24 @@ __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch
 
 // Launches a kernel that begins with pdl_wait.
 template <typename... P, typename... A>
-inline int launch_pdl(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
+inline int launch_pdl_cfg(cudaLaunchConfig_t cfg, void (*kernel)(P...), cudaStream_t stream, A... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess) return MOE_OK;
     (void)cudaGetLastError();  // reported here; later calls do not find it again
     return MOE_ERR_CUDA;
+}
+template <typename... P, typename... A>
+inline int launch_pdl(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    return launch_pdl_cfg(cfg, kernel, stream, args...);
 }
 
 }  // namespace moe

@@ -112,10 +112,6 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// silu(a) b.  The result is quantised again, so the sigmoid is a full-precision one:
-// an error of 2^-11 (tanh.approx) would move every 90th value across a rounding step.
-__device__ __forceinline__ float swiglu(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
-
 template <int EPI, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     i8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
@@ -354,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         u[i] = (float)(int)a[i] * (ws * x);
                         v[i] = (float)(int)b[i] * (ws2 * x);
                         if (EPI == I8_SWIGLU) {
-                            u[i] = swiglu(u[i], v[i]);
+                            u[i] = swiglu_f(u[i], v[i]);
                         } else {
                             u[i] += bs;
                             v[i] += bs2;
@@ -446,6 +442,7 @@ int i8_gemm_run(const I8Problem& p, cudaStream_t stream) {
     MOE_REQUIRE(!dual || aligned16(p.w2), MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE((reinterpret_cast<uintptr_t>(p.out) % dtype_size(p.out_dtype)) == 0, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(p.tile_counter, MOE_ERR_WORKSPACE);
+    if (i8_skinny_fits(p.M, p.G, p.N, p.K)) return i8_skinny_run(p, false, stream);
 
     Params kp{};
     kp.G = p.G, kp.M = p.M, kp.N = p.N, kp.offsets = p.offsets;
@@ -553,12 +550,16 @@ extern "C" int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const floa
     else p.bias = b1, p.epilogue = I8_GELU;
     int rc = i8_gemm_run(p, stream);
     if (rc != MOE_OK) return rc;
-    rc = quantize_rows(h, MOE_F32, M, F, F, hq, round16(F), hscale, offsets, G, dev_status, stream);
-    if (rc != MOE_OK) return rc;
     I8Problem d{};
     d.x = hq, d.xscale = hscale, d.M = M, d.ldx = round16(F), d.offsets = offsets, d.w = w2, d.wscale = s2;
     d.ldw = ldw2, d.bias = kind == MOE_FFN_GELU_MLP ? b2 : nullptr, d.G = G, d.N = Dout, d.K = F, d.out = ys;
     d.ldo = ldys, d.out_dtype = out_dtype, d.epilogue = I8_OUT;
     d.tile_counter = static_cast<uint32_t*>(workspace) + 16, d.status = dev_status;
+    if (i8_skinny_fits(M, G, Dout, F)) {  // which quantises the hidden rows itself
+        d.x = reinterpret_cast<const int8_t*>(h), d.ldx = F;
+        return i8_skinny_run(d, true, stream);
+    }
+    rc = quantize_rows(h, MOE_F32, M, F, F, hq, round16(F), hscale, offsets, G, dev_status, stream);
+    if (rc != MOE_OK) return rc;
     return i8_gemm_run(d, stream);
 }

@@ -34,8 +34,17 @@ struct I8Problem {
     int32_t* status;
 };
 
-// Checks sizes and alignment, encodes the tensor maps and launches.  Returns a moe_status.
+// Checks sizes and alignment and launches: the tensor-core kernel, or i8_skinny_run where i8_skinny_fits.
 int i8_gemm_run(const I8Problem& p, cudaStream_t stream);
+
+// Few rows per group: a kernel bound by the weights' bytes (i8_skinny.cu), on a problem that was checked.  f32x: p.x is
+// (M, K) fp32 (row stride ldx in values, p.xscale unused) and is quantised on the way; epilogue I8_OUT only.
+bool i8_skinny_fits(int64_t M, int G, int64_t N, int64_t K);
+int i8_skinny_run(const I8Problem& p, bool f32x, cudaStream_t stream);
+
+// silu(a) b.  The result is quantised again, so the sigmoid is a full-precision one:
+// an error of 2^-11 (tanh.approx) would move every 90th value across a rounding step.
+__device__ __forceinline__ float swiglu_f(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
 
 // Rows of x in 8 bits: all M, or with offsets (G + 1, device) those in [offsets[0], offsets[G]).
 int quantize_rows(const void* x, moe_dtype dtype, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq,
