@@ -721,37 +721,26 @@ def moe_swiglu_layer_forward(desc: SwiGLULayerDesc, x: torch.Tensor, y: torch.Te
 # Sorted rows and 8-bit products.  These calls run on the device of their tensors, whichever is current, and allocate on
 # the stream they launch on (``stream``, or that device's current one).  They take tensors as they are or refuse them:
 # nothing is copied behind the caller's back.
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(dev: torch.device, stream) -> bool:
+    """Whether the call has to change the device or the stream first; it then calls itself inside ``_there``."""
+    return stream is not None or dev.index != _current_device()
+
+
 @contextlib.contextmanager
-def _launching(dev: torch.device, stream):
+def _there(dev: torch.device, stream):
+    """Makes the device, and the stream if given, current; yields the caller's stream if it is another one."""
     with torch.cuda.device(dev):
         if stream is None:
-            yield torch._C._cuda_getCurrentRawStream(dev.index), None
+            yield None
         else:
             if stream.device != dev:
                 raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
             caller = torch.cuda.current_stream(dev)
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream, caller
-
-
-class _Here:
-    """The launch on the current device's current stream (no context to enter)."""
-
-    def __init__(self, raw):
-        self.raw = raw
-
-    def __enter__(self):
-        return self.raw, None
-
-    def __exit__(self, *exc):
-        return False
-
-
-def _launch(dev: torch.device, stream):
-    """Context giving (raw stream, the caller's stream if another one)."""
-    if stream is None and dev.index == torch._C._cuda_getDevice():
-        return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
-    return _launching(dev, stream)
+                yield caller
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -762,15 +751,16 @@ def _ptr(t: Optional[torch.Tensor]):
 def _take(name: str, t: torch.Tensor, dev: torch.device, dtype=None, shape=None, contiguous: bool = False):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor on a CUDA device")
+    if (t.device == dev and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and (not contiguous or t.is_contiguous())):
+        return t
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _ld(name: str, t: torch.Tensor, unit: int = 1) -> int:
@@ -787,11 +777,12 @@ def _ld(name: str, t: torch.Tensor, unit: int = 1) -> int:
 
 
 def _status(dev_status, dev):
-    if dev_status is not None:
-        _take("dev_status", dev_status, dev, torch.int32, contiguous=True)
-        if dev_status.numel() < 1:
-            raise ValueError("dev_status is empty")
-    return _ptr(dev_status)
+    if dev_status is None:
+        return None
+    _take("dev_status", dev_status, dev, torch.int32, contiguous=True)
+    if dev_status.numel() < 1:
+        raise ValueError("dev_status is empty")
+    return dev_status.data_ptr()
 
 
 def _scratch(nbytes: int, dev, ws):
@@ -811,15 +802,15 @@ def _keep(caller, *tensors):
     """Outputs made on another stream: the allocator waits for the caller's stream too before it reuses them."""
     if caller is not None:
         for t in tensors:
-            t.record_stream(caller)
+            if t is not None:
+                t.record_stream(caller)
 
 
-def _out(o: dict, name: str, shape, dtype, dev, fresh: list):
+def _out(o: dict, name: str, shape, dtype, dev):
     """o[name] if given (checked), else a new tensor."""
     t = o.get(name)
     if t is None:
         t = o[name] = torch.empty(*shape, dtype=dtype, device=dev)
-        fresh.append(t)
     else:
         _take(name, t, dev, dtype, shape, contiguous=True)
     return t
@@ -863,25 +854,27 @@ def moe_sort(selected: torch.Tensor, E: int, x: Optional[torch.Tensor] = None, o
         if x.dim() != 2 or x.shape[0] != T:
             raise ValueError("x must be (T, D)")
         dt, D, ldx = _dt(x), x.shape[1], _ld("x", x)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            o = moe_sort(selected, E, x, out, dev_status, workspace)
+            _keep(caller, *(t for name, t in o.items() if out is None or out.get(name) is None))
+            return o
     o = {} if out is None else dict(out)
-    fresh = []
-    with _launch(dev, stream) as (raw, caller):
-        offsets = _out(o, "offsets", (E + 1,), torch.int32, dev, fresh)
-        row = _out(o, "row", (T, k), torch.int32, dev, fresh)
-        source = _out(o, "source", (T * k,), torch.int32, dev, fresh)
-        xs = None
-        if x is not None:
-            xs = o.get("xs")
-            if xs is None:
-                xs = _out(o, "xs", (T * k, D), x.dtype, dev, fresh)
-            else:
-                _take("xs", xs, dev, x.dtype, (T * k, D))
-            ldxs = _ld("xs", xs)
-        ws = _scratch(moe_sort_workspace_size(T, k, E), dev, workspace)
-        rc = lib().moe_sort(_ptr(selected), T, k, E, _ptr(x), dt, D, ldx, _ptr(offsets), _ptr(row), _ptr(source), _ptr(xs), ldxs,
-                            _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
-        _check("moe_sort", rc)
-        _keep(caller, *fresh)
+    offsets = _out(o, "offsets", (E + 1,), torch.int32, dev)
+    row = _out(o, "row", (T, k), torch.int32, dev)
+    source = _out(o, "source", (T * k,), torch.int32, dev)
+    xs = None
+    if x is not None:
+        xs = o.get("xs")
+        if xs is None:
+            xs = o["xs"] = torch.empty(T * k, D, dtype=x.dtype, device=dev)
+            ldxs = D
+        else:
+            ldxs = _ld("xs", _take("xs", xs, dev, x.dtype, (T * k, D)))
+    ws = _scratch(lib().moe_sort_workspace_size(T, k, E), dev, workspace)
+    _check("moe_sort", lib().moe_sort(selected.data_ptr(), T, k, E, _ptr(x), dt, D, ldx, offsets.data_ptr(),
+                                      row.data_ptr(), source.data_ptr(), _ptr(xs), ldxs, _status(dev_status, dev),
+                                      _ptr(ws), _nbytes(ws), _raw_stream(dev.index)))
     return o
 
 
@@ -895,24 +888,26 @@ def moe_sort_i8(selected: torch.Tensor, E: int, x: torch.Tensor, out: Optional[d
     if x.dim() != 2 or x.shape[0] != T:
         raise ValueError("x must be (T, D)")
     dt, D, ldx = _dt(x), x.shape[1], _ld("x", x)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            o = moe_sort_i8(selected, E, x, out, dev_status, workspace)
+            _keep(caller, *(t for name, t in o.items() if out is None or out.get(name) is None))
+            return o
     o = {} if out is None else dict(out)
-    fresh = []
-    with _launch(dev, stream) as (raw, caller):
-        offsets = _out(o, "offsets", (E + 1,), torch.int32, dev, fresh)
-        row = _out(o, "row", (T, k), torch.int32, dev, fresh)
-        source = _out(o, "source", (T * k,), torch.int32, dev, fresh)
-        xscale = _out(o, "xscale", (T * k,), torch.float32, dev, fresh)
-        xq = o.get("xq")
-        if xq is None:
-            xq = o["xq"] = _padded((T * k,), D, dev)
-            fresh.append(xq)
-        else:
-            _take("xq", xq, dev, torch.int8, (T * k, D))
-        ws = _scratch(moe_sort_workspace_size(T, k, E), dev, workspace)
-        rc = lib().moe_sort_i8(_ptr(selected), T, k, E, _ptr(x), dt, D, ldx, _ptr(offsets), _ptr(row), _ptr(source), _ptr(xq),
-                               _ld("xq", xq), _ptr(xscale), _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
-        _check("moe_sort_i8", rc)
-        _keep(caller, *fresh)
+    offsets = _out(o, "offsets", (E + 1,), torch.int32, dev)
+    row = _out(o, "row", (T, k), torch.int32, dev)
+    source = _out(o, "source", (T * k,), torch.int32, dev)
+    xscale = _out(o, "xscale", (T * k,), torch.float32, dev)
+    xq = o.get("xq")
+    if xq is None:
+        xq = o["xq"] = _padded((T * k,), D, dev)
+    else:
+        _take("xq", xq, dev, torch.int8, (T * k, D))
+    ws = _scratch(lib().moe_sort_workspace_size(T, k, E), dev, workspace)
+    _check("moe_sort_i8", lib().moe_sort_i8(selected.data_ptr(), T, k, E, x.data_ptr(), dt, D, ldx, offsets.data_ptr(),
+                                            row.data_ptr(), source.data_ptr(), xq.data_ptr(), _ld("xq", xq),
+                                            xscale.data_ptr(), _status(dev_status, dev), _ptr(ws), _nbytes(ws),
+                                            _raw_stream(dev.index)))
     return o
 
 
@@ -942,15 +937,18 @@ def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor
     ldb = 0
     if base is not None:
         ldb = _ld("base", _take("base", base, dev, ys.dtype, (T, N)))
-    with _launch(dev, stream) as (raw, caller):
-        if y is None:
-            y = torch.empty(T, N, dtype=ys.dtype, device=dev)
-            _keep(caller, y)
-        else:
-            _take("y", y, dev, ys.dtype, (T, N))
-        rc = lib().moe_unsort(_ptr(ys), _ld("ys", ys), R, _ptr(row), g, gdt, T, k, N, _ptr(base), ldb, _ptr(y), _ld("y", y), dt,
-                              _status(dev_status, dev), raw)
-        _check("moe_unsort", rc)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            r = moe_unsort(ys, row, gates, base, y, dev_status)
+            _keep(caller if y is None else None, r)
+            return r
+    if y is None:
+        y = torch.empty(T, N, dtype=ys.dtype, device=dev)
+        ldy = max(N, 1)
+    else:
+        ldy = _ld("y", _take("y", y, dev, ys.dtype, (T, N)))
+    _check("moe_unsort", lib().moe_unsort(ys.data_ptr(), _ld("ys", ys), R, row.data_ptr(), g, gdt, T, k, N, _ptr(base), ldb,
+                                          y.data_ptr(), ldy, dt, _status(dev_status, dev), _raw_stream(dev.index)))
     return y
 
 
@@ -980,27 +978,29 @@ def moe_unsort_backward(dy: torch.Tensor, ys: Optional[torch.Tensor], row: torch
     elif rows is None:
         rows = T * k if dys is None else dys.shape[0]
     g, gdt = _gates(gates, dev, T, k)
-    with _launch(dev, stream) as (raw, caller):
-        fresh = []
-        if not want_dys:
-            dys = None
-        elif dys is None:
-            dys = torch.empty(rows, N, dtype=dy.dtype, device=dev)
-            fresh.append(dys)
-        else:
-            _take("dys", dys, dev, dy.dtype, (rows, N))
-        if not want_dgates:
-            dgates = None
-        elif dgates is None:
-            dgates = torch.empty(T, k, dtype=torch.float32, device=dev)
-            fresh.append(dgates)
-        else:
-            _take("dgates", dgates, dev, torch.float32, (T, k), contiguous=True)
-        rc = lib().moe_unsort_backward(_ptr(dy), _ld("dy", dy), _ptr(ys), 0 if ys is None else _ld("ys", ys), rows, _ptr(row), g,
-                                       gdt, T, k, N, _ptr(dys), 0 if dys is None else _ld("dys", dys), _ptr(dgates), dt,
-                                       _status(dev_status, dev), raw)
-        _check("moe_unsort_backward", rc)
-        _keep(caller, *fresh)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            r = moe_unsort_backward(dy, ys, row, gates, rows, want_dys, want_dgates, dys, dgates, dev_status)
+            _keep(caller, None if dys is not None else r[0], None if dgates is not None else r[1])
+            return r
+    ldd = 0
+    if not want_dys:
+        dys = None
+    elif dys is None:
+        dys = torch.empty(rows, N, dtype=dy.dtype, device=dev)
+        ldd = max(N, 1)
+    else:
+        ldd = _ld("dys", _take("dys", dys, dev, dy.dtype, (rows, N)))
+    if not want_dgates:
+        dgates = None
+    elif dgates is None:
+        dgates = torch.empty(T, k, dtype=torch.float32, device=dev)
+    else:
+        _take("dgates", dgates, dev, torch.float32, (T, k), contiguous=True)
+    _check("moe_unsort_backward",
+           lib().moe_unsort_backward(dy.data_ptr(), _ld("dy", dy), _ptr(ys), 0 if ys is None else _ld("ys", ys), rows,
+                                     row.data_ptr(), g, gdt, T, k, N, _ptr(dys), ldd, _ptr(dgates), dt,
+                                     _status(dev_status, dev), _raw_stream(dev.index)))
     return dys, dgates
 
 
@@ -1019,22 +1019,21 @@ def moe_quantize_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Op
     *lead, K = x.shape
     dt = _dt(x)
     M, ldx = (lead[0], _ld("x", x)) if len(lead) == 1 else (math.prod(lead), max(K, 1))
-    with _launch(dev, stream) as (raw, caller):
-        fresh = []
-        if q is None:
-            q = _padded(lead, K, dev)
-            fresh.append(q)
-        else:
-            _take("q", q, dev, torch.int8, x.shape)
-        if scale is None:
-            scale = torch.empty(*lead, dtype=torch.float32, device=dev)
-            fresh.append(scale)
-        else:
-            _take("scale", scale, dev, torch.float32, tuple(lead), contiguous=True)
-        ldq = _ld3("q", q, 1)
-        rc = lib().moe_quantize_i8(_ptr(x), dt, M, K, ldx, _ptr(q), ldq, _ptr(scale), _status(dev_status, dev), raw)
-        _check("moe_quantize_i8", rc)
-        _keep(caller, *fresh)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            r = moe_quantize_i8(x, q, scale, dev_status)
+            _keep(caller, None if q is not None else r[0], None if scale is not None else r[1])
+            return r
+    if q is None:
+        q = _padded(lead, K, dev)
+    else:
+        _take("q", q, dev, torch.int8, x.shape)
+    if scale is None:
+        scale = torch.empty(*lead, dtype=torch.float32, device=dev)
+    else:
+        _take("scale", scale, dev, torch.float32, tuple(lead), contiguous=True)
+    _check("moe_quantize_i8", lib().moe_quantize_i8(x.data_ptr(), dt, M, K, ldx, q.data_ptr(), _ld3("q", q, 1),
+                                                    scale.data_ptr(), _status(dev_status, dev), _raw_stream(dev.index)))
     return q, scale
 
 
@@ -1042,6 +1041,10 @@ def _ld3(name: str, t: torch.Tensor, unit: int) -> int:
     """The one row stride of a tensor (..., N, K) whose rows lie evenly; a single row's is rounded up to ``unit``."""
     if t.dim() == 2:
         return _ld(name, t, unit)
+    if t.dim() == 3:  # the usual case first
+        (G, N, K), (between, ld, step) = t.shape, t.stride()
+        if step == 1 and N > 1 and ld >= K and (G == 1 or between == N * ld):
+            return ld
     K = t.shape[-1]
     if K > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit column stride")
@@ -1067,7 +1070,7 @@ def _weight_i8(name, w, scale, dev, G, N, K):
     _take(name, w, dev, torch.int8)
     if w.shape != (G, N, K) and (G != 1 or w.shape != (N, K)):
         raise ValueError(f"{name} must be ({G}, {N}, {K}), got {tuple(w.shape)}")
-    _take(f"{name}'s scale", scale, dev, torch.float32, contiguous=True)
+    _take("the weight's scale", scale, dev, torch.float32, None, True)
     if scale.numel() != G * N:
         raise ValueError(f"{name} needs {G * N} scales, got {scale.numel()}")
     return _ld3(name, w, 16)
@@ -1121,16 +1124,20 @@ def moe_matmul_i8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wsca
     ldw = _weight_i8("wq", wq, wscale, dev, G, N, K)
     b = _bias_i8("bias", bias, dev, G, N)
     dtype, dt = _out_dt(out, out_dtype)
-    with _launch(dev, stream) as (raw, caller):
-        if out is None:
-            out = torch.empty(M, N, dtype=dtype, device=dev)
-            _keep(caller, out)
-        else:
-            _take("out", out, dev, dtype, (M, N))
-        ws = _scratch(int(lib().moe_matmul_i8_workspace_size(M, G, N, K)), dev, workspace)
-        rc = lib().moe_matmul_i8(_ptr(xq), _ptr(xscale), M, _ld("xq", xq, 16), _ptr(offsets), _ptr(wq), _ptr(wscale), ldw, b, G, N, K,
-                                 _ptr(out), _ld("out", out), dt, _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
-        _check("moe_matmul_i8", rc)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            r = moe_matmul_i8(xq, xscale, wq, wscale, offsets, bias, out, out_dtype, dev_status, workspace)
+            _keep(caller if out is None else None, r)
+            return r
+    if out is None:
+        out = torch.empty(M, N, dtype=dtype, device=dev)
+        ldo = max(N, 1)
+    else:
+        ldo = _ld("out", _take("out", out, dev, dtype, (M, N)))
+    ws = _scratch(lib().moe_matmul_i8_workspace_size(M, G, N, K), dev, workspace)
+    _check("moe_matmul_i8", lib().moe_matmul_i8(xq.data_ptr(), xscale.data_ptr(), M, _ld("xq", xq, 16), _ptr(offsets),
+                                                wq.data_ptr(), wscale.data_ptr(), ldw, b, G, N, K, out.data_ptr(), ldo, dt,
+                                                _status(dev_status, dev), _ptr(ws), _nbytes(ws), _raw_stream(dev.index)))
     return out
 
 
@@ -1179,17 +1186,23 @@ def moe_expert_ffn_i8(kind: str, xq: torch.Tensor, xscale: torch.Tensor, offsets
         raise ValueError("w3 belongs to SwiGLU experts")
     pb1, pb2 = _bias_i8("b1", b1, dev, G, n1), _bias_i8("b2", b2, dev, G, Dout)
     dtype, dt = _out_dt(ys, out_dtype)
-    with _launch(dev, stream) as (raw, caller):
-        if ys is None:
-            ys = torch.empty(M, Dout, dtype=dtype, device=dev)
-            _keep(caller, ys)
-        else:
-            _take("ys", ys, dev, dtype, (M, Dout))
-        ws = _scratch(moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout), dev, workspace)
-        rc = lib().moe_expert_ffn_i8(FFN[kind], _ptr(xq), _ptr(xscale), M, _ld("xq", xq, 16), _ptr(offsets), G, D, F, Dout,
-                                     _ptr(w1), _ptr(s1), ld1, pb1, _ptr(w2), _ptr(s2), ld2, pb2, _ptr(w3), _ptr(s3), _ptr(ys),
-                                     _ld("ys", ys), dt, _status(dev_status, dev), _ptr(ws), _nbytes(ws), raw)
-        _check("moe_expert_ffn_i8", rc)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream) as caller:
+            r = moe_expert_ffn_i8(kind, xq, xscale, offsets, w1, s1, b1, w2, s2, b2, w3, s3, ys, out_dtype, dev_status,
+                                  workspace)
+            _keep(caller if ys is None else None, r)
+            return r
+    if ys is None:
+        ys = torch.empty(M, Dout, dtype=dtype, device=dev)
+        ldy = max(Dout, 1)
+    else:
+        ldy = _ld("ys", _take("ys", ys, dev, dtype, (M, Dout)))
+    ws = _scratch(lib().moe_expert_ffn_i8_workspace_size(FFN[kind], G, M, D, F, Dout), dev, workspace)
+    _check("moe_expert_ffn_i8",
+           lib().moe_expert_ffn_i8(FFN[kind], xq.data_ptr(), xscale.data_ptr(), M, _ld("xq", xq, 16), _ptr(offsets), G, D, F,
+                                   Dout, w1.data_ptr(), s1.data_ptr(), ld1, pb1, _ptr(w2), _ptr(s2), ld2, pb2, _ptr(w3),
+                                   _ptr(s3), ys.data_ptr(), ldy, dt, _status(dev_status, dev), _ptr(ws), _nbytes(ws),
+                                   _raw_stream(dev.index)))
     return ys
 
 

@@ -441,8 +441,8 @@ int i8_gemm_run(const I8Problem& p, cudaStream_t stream) {
                 MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE(!dual || aligned16(p.w2), MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE((reinterpret_cast<uintptr_t>(p.out) % dtype_size(p.out_dtype)) == 0, MOE_ERR_INVALID_ARG);
-    MOE_REQUIRE(p.tile_counter, MOE_ERR_WORKSPACE);
     if (i8_skinny_fits(p.M, p.G, p.N, p.K)) return i8_skinny_run(p, false, stream);
+    MOE_REQUIRE(p.tile_counter, MOE_ERR_WORKSPACE);
 
     Params kp{};
     kp.G = p.G, kp.M = p.M, kp.N = p.N, kp.offsets = p.offsets;
@@ -491,15 +491,15 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 }  // namespace
 
 extern "C" size_t moe_matmul_i8_workspace_size(int64_t M, int32_t G, int64_t N, int64_t K) {
-    return M < 1 || G < 1 || N < 1 || K < 1 ? 0 : kCounterBytes;
+    return M < 1 || G < 1 || N < 1 || K < 1 || i8_skinny_fits(M, G, N, K) ? 0 : kCounterBytes;
 }
 
 extern "C" int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, int64_t ldx, const int32_t* offsets,
                              const int8_t* wq, const float* wscale, int64_t ldw, const float* bias, int32_t G,
                              int64_t N, int64_t K, void* out, int64_t ldo, moe_dtype out_dtype, int32_t* dev_status,
                              void* workspace, size_t workspace_bytes, moe_stream_t stream) {
-    MOE_REQUIRE(M < 1 || (workspace && workspace_bytes >= moe_matmul_i8_workspace_size(M, G, N, K)),
-                MOE_ERR_WORKSPACE);
+    const size_t need = moe_matmul_i8_workspace_size(M, G, N, K);
+    MOE_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), MOE_ERR_WORKSPACE);
     I8Problem p{};
     p.x = xq, p.xscale = xscale, p.M = M, p.ldx = ldx, p.offsets = offsets, p.w = wq, p.wscale = wscale;
     p.ldw = ldw, p.bias = bias, p.G = G, p.N = N, p.K = K, p.out = out, p.ldo = ldo, p.out_dtype = out_dtype;
