@@ -5,18 +5,26 @@
 //
 // The weights are on the MMA's M side, so that a group's row count sets the MMA's N and
 // a ragged expert wastes at most 31 token rows.  Two CTAs on two SMs share each MMA of
-// 256 weight rows x up to 256 tokens, and a tile has two accumulators on the same
-// tokens: 512 output features of one weight, or 256 features of gate and up (SwiGLU).
-// Per 128-deep K block that is 48 KB of shared memory per SM (two weight tiles of
-// 16 KB, half of the tokens) for 2 x 128 x 256 x 128 products, and four stages fit.
-// The accumulators fill all 512 TMEM columns.
+// 256 weight rows x up to 256 tokens: 256 output features, or 128 of gate and up (SwiGLU;
+// 64 rows of each per CTA, so that one warp has a feature's gate and another one its up, and
+// they exchange them through shared memory.  16 rows of each in turn would put both into
+// one warp's TMEM lanes, but the TMA copy of so many small boxes takes longer than the
+// MMAs, at 70 cycles each).  Per 128-deep K block that is 32 KB of shared memory per SM,
+// and five stages fit.  The two
+// halves of TMEM hold two tiles' accumulators, so a tile's epilogue runs under the next
+// one's MMAs.  (Two accumulators on the same tokens would need 24 KB a block and MMA, but
+// the epilogue then stands alone: 2.2 us of MMAs and 8 us of epilogue per tile at K = 512.)
 //
 // Warp roles (576 threads per CTA, one persistent CTA per SM):
-//   warp 0      TMA producer; the even CTA's draws tiles from a global counter and hands
-//               each index to both CTAs through a small queue
-//   warp 1      TMEM owner and MMA issuer (one lane of the even CTA)
-//   warps 2-17  epilogue: warp w drains TMEM lanes 32 (w % 4).. (32 features of each
-//               accumulator) for the 64 tokens [64 r, 64 r + 64), r = (w - 2) / 4
+//   warp 0      TMA producer
+//   warp 1      TMEM owner; in the even CTA one lane issues the MMAs, in the odd one it hands
+//               out tiles to both CTAs through a small queue, in turn or, where groups make
+//               them uneven, from a global counter (finding a tile's group takes as long as
+//               one of its K blocks, so no other role does it)
+//   warps 2-17  epilogue: warp w drains TMEM lanes 32 (w % 4).. for the 64 tokens
+//               [64 r, 64 r + 64), r = (w - 2) / 4.  16-bit results are transposed through
+//               shared memory (stmatrix) and written 64 bytes per token.  The next tile's
+//               scales are on their way while one is worked on.
 // Every wait is bounded (kWaitLimitNs); after a timeout nothing more is written.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -37,18 +45,18 @@ constexpr int kM = 128;        // features per CTA and accumulator (half of the 
 constexpr int kBK = 128;       // K per stage: one 128-byte swizzle row
 constexpr int kNT = 256;       // most tokens per tile (MMA N)
 constexpr int kBox = 32;       // token rows per TMA box
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kMaxGroups = 2048;
 constexpr int kQueue = 4;      // tile indices in flight between the producer and the consumers
 constexpr int kWBytes = kM * kBK;
 constexpr int kXBytes = (kNT / 2) * kBK;
-constexpr int kStageBytes = 2 * kWBytes + kXBytes;
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 256;
-// consumers of a queue slot, all counted on the even CTA: its MMA issuer and
-// epilogue warps, the odd CTA's producer and epilogue warps
-constexpr int kQueueConsumers = 1 + kEpiWarps + 1 + kEpiWarps;
+constexpr int kStageBytes = kWBytes + kXBytes;
+constexpr int kStoreBytes = 32 * 32 * 2;  // per epilogue warp: 32 tokens x 32 features of 16 bits, or 16 x 32 of 32
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kStoreBytes + 256;
+// consumers of a queue slot, all counted on the odd CTA: both producers, the MMA issuer and both CTAs' epilogue warps
+constexpr int kQueueConsumers = 2 + 1 + 2 * kEpiWarps;
 
 struct Params {
     int G;
@@ -58,12 +66,14 @@ struct Params {
     const float* wscale;
     const float* wscale2;
     const float* bias;
-    int tile_f;   // output features per tile: 512, or 256 for SwiGLU
+    int tile_f;   // output features per tile: 256, or 128 for SwiGLU
     int f_tiles;
     int k_blocks;
+    int max_span; // most tokens per tile
+    bool vec_out; // rows of out start on 16 bytes
     void* out;
     int64_t ldo;
-    uint32_t* tile_counter;  // zero at launch: the next tile to hand out
+    uint32_t* tile_counter;  // zero at launch: the next tile to hand out; NULL: every pair's in turn
     int32_t* status;
 };
 
@@ -73,10 +83,10 @@ __device__ __forceinline__ int row_offset(const Params& p, int g) {
     return o < 0 ? 0 : (o > p.M ? (int)p.M : o);
 }
 
-// A group's rows split into ceil(rows / 256) tiles of equal size (a multiple of the TMA box).
-__device__ __forceinline__ int token_span(int rows) {
-    const int n_tt = (rows + kNT - 1) / kNT;
-    if (n_tt <= 0) return kNT;
+// A group's rows split into ceil(rows / max_span) tiles of equal size (a multiple of the TMA box).
+__device__ __forceinline__ int token_span(int rows, int max_span) {
+    const int n_tt = (rows + max_span - 1) / max_span;
+    if (n_tt <= 0) return max_span;
     const int span = (rows + n_tt - 1) / n_tt;
     return (span + kBox - 1) / kBox * kBox;
 }
@@ -84,53 +94,71 @@ __device__ __forceinline__ int token_span(int rows) {
 // the tokens of one CTA: a tile's n tokens in two halves of a multiple of 16
 __device__ __forceinline__ int token_half(int n) { return ((n + 1) / 2 + 15) / 16 * 16; }
 
-struct Tile {
-    int g, ft, row0, n;  // group, feature tile, first row of X, rows
+struct __align__(16) Tile {
+    int g, ft, row0, n;  // group (-1: no more tiles), feature tile, first row of X, rows
 };
 
-// Feature tiles fastest, so that tiles which run together share the group's tokens.
-__device__ __forceinline__ Tile decode(int tile, const int* prefix, const int* off, const Params& p) {
-    int lo = 0, hi = p.G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= tile) lo = mid;
-        else hi = mid - 1;
+// The tile's place, found by the 32 lanes of a warp together.  Feature tiles fastest, so that tiles which run together
+// share the group's tokens.
+__device__ __forceinline__ Tile decode(int tile, const int* prefix, const int* off, const Params& p, int lane) {
+    // the last group whose first tile is not behind this one: a 32nd of the groups, then the group
+    const int stride = (p.G + 31) / 32;
+    const int probe = lane * stride;
+    const int part = __popc(__ballot_sync(0xffffffffu, probe < p.G && prefix[probe] <= tile)) - 1;
+    int g = part * stride - 1;
+    for (int i = 0; i < stride; i += 32) {
+        const int at = part * stride + i + lane;
+        g += __popc(__ballot_sync(0xffffffffu, i + lane < stride && at < p.G && prefix[at] <= tile));
     }
     Tile t;
-    t.g = lo;
-    const int local = tile - prefix[lo];
+    t.g = g;
+    const int local = tile - prefix[g];
     const int tt = local / p.f_tiles;
     t.ft = local - tt * p.f_tiles;
-    const int rows = off[lo + 1] - off[lo];
-    const int span = token_span(rows);
-    t.row0 = off[lo] + tt * span;
+    const int rows = off[g + 1] - off[g];
+    const int span = token_span(rows, p.max_span);
+    t.row0 = off[g] + tt * span;
     t.n = rows - tt * span < span ? rows - tt * span : span;
     return t;
 }
 
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, int v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_cluster_tile(uint32_t addr, const Tile& t) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(t.g), "r"(t.ft), "r"(t.row0), "r"(t.n)
+                 : "memory");
+}
+
+// Takes a tile from this CTA's copy of a queue slot; one thread per consumer.
+__device__ __forceinline__ Tile take_tile(uint64_t* qfull, const Tile* slots, uint32_t qempty_l, uint32_t it, int32_t* status,
+                                          volatile int* abort) {
+    const uint32_t slot = it % kQueue;
+    Tile t;
+    t.g = -1;
+    if (mbar_wait_cluster(&qfull[slot], (it / kQueue) & 1u, status)) t = slots[slot];
+    else *abort = 1;
+    mbar_arrive_cluster_relaxed(qempty_l + 8u * slot, (uint32_t)(t.g ^ t.ft ^ t.row0 ^ t.n));
+    return t;
 }
 
 template <int EPI, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     i8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
-              const __grid_constant__ CUtensorMap tmX, const Params p) {
+              const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX128, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_prefix[kMaxGroups + 1];
     __shared__ int s_off[kMaxGroups + 1];
-    __shared__ int s_tile[kQueue];
+    __shared__ Tile s_tile[kQueue];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint8_t* store = smem + kStages * kStageBytes;  // the epilogue warps' transposed chunks
+    uint64_t* bars = reinterpret_cast<uint64_t*>(store + kEpiWarps * kStoreBytes);
     uint64_t* full = bars;                // even CTA: a stage's loads of both CTAs have landed
     uint64_t* empty = bars + kStages;     // both CTAs: the stage's MMAs are done
-    uint64_t* tfull = bars + 2 * kStages; // both CTAs: the accumulators hold a finished tile
-    uint64_t* tempty = tfull + 1;         // even CTA: both epilogues drained the accumulators
-    uint64_t* qfull = tempty + 1;         // both CTAs: s_tile[q] holds the next tile
-    uint64_t* qempty = qfull + kQueue;    // even CTA: every consumer has read s_tile[q]
+    uint64_t* tfull = bars + 2 * kStages; // both CTAs: an accumulator holds a finished tile
+    uint64_t* tempty = tfull + 2;         // even CTA: both epilogues drained the accumulator
+    uint64_t* qfull = tempty + 2;         // both CTAs: s_tile[q] holds the next tile
+    uint64_t* qempty = qfull + kQueue;    // odd CTA: every consumer has read s_tile[q]
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -142,8 +170,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(tfull, 1);
-        mbar_init(tempty, 2 * kEpiWarps);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], 2 * kEpiWarps);
+        }
         for (int q = 0; q < kQueue; ++q) {
             mbar_init(&qfull[q], 1);
             mbar_init(&qempty[q], kQueueConsumers);
@@ -160,13 +190,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    pdl_wait();
+    pdl_next();
     // tiles before each group; offsets that run backwards leave the group empty
     for (int g = threadIdx.x; g <= p.G; g += kThreads) s_off[g] = row_offset(p, g);
     __syncthreads();
     for (int g = threadIdx.x; g < p.G; g += kThreads) {
         const int r = s_off[g + 1] - s_off[g];
         if (r < 0) set_status(p.status, MOE_ERR_BAD_INDEX);
-        s_prefix[g] = r > 0 ? (r + token_span(r) - 1) / token_span(r) * p.f_tiles : 0;
+        const int span = token_span(r, p.max_span);
+        s_prefix[g] = r > 0 ? (r + span - 1) / span * p.f_tiles : 0;
     }
     __syncthreads();
     block_scan<kThreads>(s_prefix, p.G);
@@ -175,48 +208,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const int total = s_prefix[p.G];
     const uint32_t tmem_base = s_tmem;
-    // the even CTA's barriers as shared::cluster addresses
+    // barriers of the even, and the odd CTA as shared::cluster addresses
     const uint32_t full_l = mapa_shared(smem_u32(full), 0);
     const uint32_t tempty_l = mapa_shared(smem_u32(tempty), 0);
-    const uint32_t qempty_l = mapa_shared(smem_u32(qempty), 0);
+    const uint32_t qempty_l = mapa_shared(smem_u32(qempty), 1);
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            for (int i = 0;; ++i) {
-                const int q = i % kQueue;
-                const uint32_t qph = (uint32_t)(i / kQueue) & 1u;
-                int tile;
-                if (leader) {
-                    if (!mbar_wait_cluster(&qempty[q], qph ^ 1u, p.status)) {
-                        s_abort = 1;
-                        tile = -1;
-                    } else {
-                        tile = s_abort ? -1 : (int)atomicAdd(p.tile_counter, 1u);
-                        if (tile >= total) tile = -1;
-                    }
-                    s_tile[q] = tile;
-                    st_cluster_u32(mapa_shared(smem_u32(&s_tile[q]), 1), tile);
-                    mbar_arrive(&qfull[q]);
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&qfull[q]), 1));  // release: orders the store
-                } else {
-                    tile = -1;
-                    if (mbar_wait_cluster(&qfull[q], qph, p.status)) tile = s_tile[q];
-                    else s_abort = 1;
-                    mbar_arrive_cluster(qempty_l + 8u * (uint32_t)q);
-                }
-                if (tile < 0) break;
-                const Tile t = decode(tile, s_prefix, s_off, p);
+            for (uint32_t it = 0;; ++it) {
+                const Tile t = take_tile(qfull, s_tile, qempty_l, it, p.status, &s_abort);
+                if (t.g < 0) break;
                 const int half = token_half(t.n);
                 const int nbox = (half + kBox - 1) / kBox;
-                const int64_t f0 = (int64_t)t.ft * p.tile_f + (int64_t)rank * kM;
-                const int32_t w_y = (int32_t)(t.g * p.N + f0);
-                const bool two = EPI == I8_SWIGLU || (int64_t)t.ft * p.tile_f + 2 * kM < p.N;
-                const int32_t w_y2 = EPI == I8_SWIGLU ? w_y : w_y + 2 * kM;
+                const int32_t w_y = (int32_t)(t.g * p.N + (int64_t)t.ft * p.tile_f + (int64_t)rank * (p.tile_f / 2));
                 const int32_t x_y = t.row0 + (int32_t)rank * half;
-                const uint32_t tx_pair = 2u * (uint32_t)((two ? 2 : 1) * kWBytes + nbox * kBox * kBK);
+                const uint32_t tx_pair = 2u * (uint32_t)(kWBytes + nbox * kBox * kBK);
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, p.status)) {
                         s_abort = 1;
@@ -226,9 +235,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t fb = full_l + 8u * (uint32_t)stage;
                     uint8_t* st = smem + stage * kStageBytes;
                     tma_load_2d_pair(st, &tmW, kb * kBK, w_y, fb);
-                    if (two) tma_load_2d_pair(st + kWBytes, &tmW2, kb * kBK, w_y2, fb);
-                    for (int b = 0; b < nbox; ++b)
-                        tma_load_2d_pair(st + 2 * kWBytes + b * (kBox * kBK), &tmX, kb * kBK, x_y + b * kBox, fb);
+                    if (EPI == I8_SWIGLU) tma_load_2d_pair(st + kWBytes / 2, &tmW2, kb * kBK, w_y, fb);
+                    if (nbox == 4)
+                        tma_load_2d_pair(st + kWBytes, &tmX128, kb * kBK, x_y, fb);
+                    else
+                        for (int b = 0; b < nbox; ++b)
+                            tma_load_2d_pair(st + kWBytes + b * (kBox * kBK), &tmX, kb * kBK, x_y + b * kBox, fb);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -244,18 +256,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             bool ready = false;  // full[stage] was seen complete by an early test
             for (uint32_t it = 0;; ++it) {
-                const int q = (int)(it % kQueue);
-                if (!mbar_wait(&qfull[q], (it / kQueue) & 1u, p.status)) {
-                    s_abort = 1;
-                    break;
-                }
-                const int tile = s_tile[q];
-                mbar_arrive(&qempty[q]);
-                if (tile < 0) break;
-                const Tile t = decode(tile, s_prefix, s_off, p);
+                const Tile t = take_tile(qfull, s_tile, qempty_l, it, p.status, &s_abort);
+                if (t.g < 0) break;
                 const uint32_t idesc = make_idesc_i8(2 * kM, 2 * token_half(t.n));
-                const bool two = EPI == I8_SWIGLU || (int64_t)t.ft * p.tile_f + 2 * kM < p.N;
-                if (!mbar_wait_cluster(tempty, (it & 1u) ^ 1u, p.status)) {
+                const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
+                if (!mbar_wait_cluster(&tempty[acc], aph ^ 1u, p.status)) {
                     s_abort = 1;
                     break;
                 }
@@ -268,15 +273,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + stage * kStageBytes);
-                    const uint64_t wd = sw128_desc(st), wd2 = sw128_desc(st + kWBytes);
-                    const uint64_t xd = sw128_desc(st + 2 * kWBytes);
+                    const uint64_t wd = sw128_desc(st), xd = sw128_desc(st + kWBytes);
                     const int ns = stage + 1 == kStages ? 0 : stage + 1;
                     const uint32_t np = stage + 1 == kStages ? phase ^ 1u : phase;
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk) {
                         const uint32_t accum = (kb > 0 || kk > 0) ? 1u : 0u;
-                        tc_mma_i8_pair(tmem_base, wd + 2 * kk, xd + 2 * kk, idesc, accum);
-                        if (two) tc_mma_i8_pair(tmem_base + 256, wd2 + 2 * kk, xd + 2 * kk, idesc, accum);
+                        tc_mma_i8_pair(tmem_base + acc * kNT, wd + 2 * kk, xd + 2 * kk, idesc, accum);
                         // the tensor core takes new MMAs only as it finishes old ones: look at the
                         // next stage while this one's MMAs are being accepted
                         if (kk == 1) ready = mbar_test(smem_u32(&full[ns]), np);
@@ -289,114 +292,213 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     s_abort = 1;
                     break;
                 }
-                tc_commit_pair(tfull);
+                tc_commit_pair(&tfull[acc]);
+            }
+        } else if (!leader) {
+            // ------------------------------ tile scheduler ----------------------------
+            const int step = p.tile_counter ? 0 : (int)(gridDim.x / 2);
+            int ahead = (int)(blockIdx.x / 2);  // the next tile; from the counter it is asked for one tile early
+            if (!step && lane == 0) ahead = (int)atomicAdd(p.tile_counter, 1u);
+            for (int i = 0;; ++i) {
+                const int q = i % kQueue;
+                int tile = __shfl_sync(0xffffffffu, ahead, 0);
+                if (step) ahead += step;
+                else if (lane == 0 && tile < total) ahead = (int)atomicAdd(p.tile_counter, 1u);
+                Tile t;
+                t.g = t.ft = t.row0 = t.n = -1;
+                if (tile < total) t = decode(tile, s_prefix, s_off, p, lane);
+                if (lane == 0) {
+                    if (!mbar_wait_cluster(&qempty[q], ((uint32_t)(i / kQueue) & 1u) ^ 1u, p.status)) s_abort = 1;
+                    if (s_abort) t.g = -1;
+                    s_tile[q] = t;
+                    st_cluster_tile(mapa_shared(smem_u32(&s_tile[q]), 0), t);
+                    mbar_arrive(&qfull[q]);
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&qfull[q]), 0));  // release: orders the store
+                }
+                if (__shfl_sync(0xffffffffu, t.g, 0) < 0) break;
             }
         }
         __syncwarp();
     } else {
         // -------------------------------- epilogue --------------------------------
-        const int q = warp & 3;          // TMEM lane quarter: features 32q .. 32q+31 of this CTA's 128
+        const int q = warp & 3;          // TMEM lane quarter: weight rows 32q .. 32q+31 of this CTA's 128
         const int r = (warp - 2) >> 2;   // token quarter: tokens 64r .. 64r+63 of the tile
-        const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-        for (uint32_t it = 0;; ++it) {
-            const int q_slot = (int)(it % kQueue);
-            int tile = -1;
-            if (lane == 0) {
-                if (mbar_wait_cluster(&qfull[q_slot], (it / kQueue) & 1u, p.status)) tile = s_tile[q_slot];
-                else s_abort = 1;
-                mbar_arrive_cluster(qempty_l + 8u * (uint32_t)q_slot);
+        const int gl = lane >> 2, c2 = 2 * (lane & 3);  // row and first column of this lane in an 8 x 8 block
+        const bool up = EPI == I8_SWIGLU && q >= 2;
+        uint8_t* stage_out = store + (warp - 2) * kStoreBytes;
+        // What a tile's epilogue needs besides the sums.
+        struct Work {
+            Tile t;
+            int64_t f0;          // the features of this warp's weight rows: 32 from here
+            float ws[4], bs[4];  // scales and biases of rows gl, gl + 8, gl + 16, gl + 24
+            float xs[2];         // scales of tokens 64 r + lane, 64 r + 32 + lane
+        };
+        const auto take = [&](uint32_t it) {
+            Work w;
+            if (lane == 0) w.t = take_tile(qfull, s_tile, qempty_l, it, p.status, &s_abort);
+            w.t.g = __shfl_sync(0xffffffffu, w.t.g, 0);
+            if (w.t.g < 0) return w;
+            w.t.ft = __shfl_sync(0xffffffffu, w.t.ft, 0);
+            w.t.row0 = __shfl_sync(0xffffffffu, w.t.row0, 0);
+            w.t.n = __shfl_sync(0xffffffffu, w.t.n, 0);
+            w.f0 = (int64_t)w.t.ft * p.tile_f + (int64_t)rank * (p.tile_f / 2) + (EPI == I8_SWIGLU ? q & 1 : q) * 32;
+            const float* scales = up ? p.wscale2 : p.wscale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t f = w.f0 + gl + 8 * i;
+                w.ws[i] = f < p.N ? scales[w.t.g * p.N + f] : 0.f;
+                w.bs[i] = EPI != I8_SWIGLU && p.bias && f < p.N ? p.bias[w.t.g * p.N + f] : 0.f;
             }
-            tile = __shfl_sync(0xffffffffu, tile, 0);
-            if (tile < 0) break;
-            const Tile t = decode(tile, s_prefix, s_off, p);
-            // this thread's features, their scales, and the scales of this warp's tokens
-            const int64_t f = (int64_t)t.ft * p.tile_f + (int64_t)rank * kM + q * 32 + lane;
-            const int64_t f2 = EPI == I8_SWIGLU ? f : f + 2 * kM;
-            float ws = 0.f, ws2 = 0.f, bs = 0.f, bs2 = 0.f;
-            if (f < p.N) ws = p.wscale[t.g * p.N + f];
-            if (f2 < p.N) ws2 = (EPI == I8_SWIGLU ? p.wscale2 : p.wscale)[t.g * p.N + f2];
-            if (EPI != I8_SWIGLU && p.bias) {
-                if (f < p.N) bs = p.bias[t.g * p.N + f];
-                if (f2 < p.N) bs2 = p.bias[t.g * p.N + f2];
-            }
-            float xs[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int tok = 64 * r + 32 * h + lane;
-                xs[h] = tok < t.n ? p.xscale[t.row0 + tok] : 0.f;
+                w.xs[h] = tok < w.t.n ? p.xscale[w.t.row0 + tok] : 0.f;
             }
+            return w;
+        };
+        Work cur = take(0);
+        for (uint32_t it = 0; cur.t.g >= 0; ++it) {
+            const Work next = take(it + 1);
+            const Tile& t = cur.t;
+            const uint32_t acc = it & 1u;
             int ok = 1;
-            if (lane == 0) ok = mbar_wait(tfull, it & 1u, p.status) ? 1 : 0;
+            if (lane == 0) ok = mbar_wait(&tfull[acc], (it >> 1) & 1u, p.status) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) s_abort = 1;
             tc_fence_after();
             const bool live = !s_abort;
-            TO* out = static_cast<TO*>(p.out) + (int64_t)(t.row0 + 64 * r) * p.ldo;
-            constexpr bool kPacked = sizeof(TO) == 2;  // bf16 results wait in registers until TMEM is released
-            uint32_t h1[4][8], h2[4][8];
-
+            const int left = t.n - 64 * r;  // tokens from this warp's first on
+            const uint32_t tmem = tmem_base + acc * kNT + ((uint32_t)(q * 32) << 16) + (uint32_t)(64 * r);
+            // The warp's columns are in registers (tcgen05.wait::ld): hand the accumulator back.
+            const auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(tempty_l + 8u * acc, 0);
+            };
+            // v[i][j][e]: row gl + 8 i, token 16 c + 8 j + c2 + e of this warp's 64
+            const auto sums = [&](int c, float (&v)[4][2][2]) {
+                uint32_t raw[16];
+                tmem_ld_32x16(tmem + 16u * (uint32_t)c, raw);
+                tmem_ld_wait(raw);
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                const int tok0 = 64 * r + 16 * ch;
-                if (tok0 < t.n) {
-                    uint32_t a[16], b[16];
-                    tmem_ld16(tmem_base + lane_off + (uint32_t)tok0, a);
-                    tmem_ld16(tmem_base + 256 + lane_off + (uint32_t)tok0, b);
-                    tmem_ld_wait(a, b);
-                    float u[16], v[16];
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = __shfl_sync(0xffffffffu, xs[ch >> 1], (16 * ch + i) & 31);
-                        u[i] = (float)(int)a[i] * (ws * x);
-                        v[i] = (float)(int)b[i] * (ws2 * x);
-                        if (EPI == I8_SWIGLU) {
-                            u[i] = swiglu_f(u[i], v[i]);
-                        } else {
-                            u[i] += bs;
-                            v[i] += bs2;
-                        }
-                        if (EPI == I8_GELU) {
-                            u[i] = gelu_f(u[i]);
-                            v[i] = gelu_f(v[i]);
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = __shfl_sync(0xffffffffu, c < 2 ? cur.xs[0] : cur.xs[1], (16 * c + 8 * j + c2 + e) & 31);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i][j][e] = (float)(int)raw[8 * (i >> 1) + 4 * j + 2 * (i & 1) + e] * (cur.ws[i] * x);
+                    }
+            };
+            // eight lanes of consecutive features: a whole sector
+            const auto put = [&](int c, const float (&v)[4][2][2]) {
+                if (!live) return;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int tok = 16 * c + 8 * j + c2 + e;
+                        if (tok >= left) continue;
+                        TO* dst = static_cast<TO*>(p.out) + (int64_t)(t.row0 + 64 * r + tok) * p.ldo + cur.f0 + gl;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (cur.f0 + gl + 8 * i < p.N) dst[8 * i] = from_f32<TO>(v[i][j][e]);
+                    }
+            };
+            if (left <= 0) {
+                release();
+            } else if constexpr (EPI == I8_SWIGLU) {
+                // The gate's warp finishes the first 32 tokens, the up's the other 32: each gives the other one 16 tokens'
+                // products at a time, lane to lane.
+                const int mine = up ? 2 : 0, other = 2 - mine;
+                uint4* give = reinterpret_cast<uint4*>(stage_out) + lane;
+                const uint4* get = reinterpret_cast<const uint4*>(store + (warp - 2 + (up ? 2 : -2)) * kStoreBytes) + lane;
+                const int bar = 1 + 2 * r + (q & 1);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    float v[4][2][2], w[4][2][2];
+                    if (16 * (other + s) < left) {
+                        sums(other + s, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            give[32 * i] = make_uint4(__float_as_uint(v[i][0][0]), __float_as_uint(v[i][0][1]),
+                                                      __float_as_uint(v[i][1][0]), __float_as_uint(v[i][1][1]));
+                    }
+                    const bool own = 16 * (mine + s) < left;
+                    if (own) sums(mine + s, v);
+                    if (s == 1) release();
+                    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+                    if (own) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 u = get[32 * i];
+                            w[i][0][0] = __uint_as_float(u.x), w[i][0][1] = __uint_as_float(u.y);
+                            w[i][1][0] = __uint_as_float(u.z), w[i][1][1] = __uint_as_float(u.w);
                         }
                     }
-                    if (kPacked) {
+                    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // the partner's buffer is read
+                    if (own) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            h1[ch][i] = pack_bf16x2(u[2 * i], u[2 * i + 1]);
-                            if (EPI != I8_SWIGLU) h2[ch][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                        }
-                    } else if (live) {
-                        TO* dst = out + (int64_t)16 * ch * p.ldo;
-                        const int n = t.n - tok0 < 16 ? t.n - tok0 : 16;
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < n) {
-                                if (f < p.N) dst[i * p.ldo + f] = from_f32<TO>(u[i]);
-                                if (EPI != I8_SWIGLU && f2 < p.N) dst[i * p.ldo + f2] = from_f32<TO>(v[i]);
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    v[i][j][e] = up ? swiglu_f(w[i][j][e], v[i][j][e]) : swiglu_f(v[i][j][e], w[i][j][e]);
+                        put(mine + s, v);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (16 * c >= left) continue;
+                    float v[4][2][2];
+                    sums(c, v);
+                    if (c == 3 || left <= 16 * (c + 1)) release();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                v[i][j][e] += cur.bs[i];
+                                if (EPI == I8_GELU) v[i][j][e] = gelu_f(v[i][j][e]);
                             }
+                    if constexpr (sizeof(TO) == 4) {
+                        put(c, v);
+                    } else {
+                        // 32 tokens at a time: lane 8 m + k addresses token 8 j + k, features 8 m ..; the 16-byte pieces are
+                        // swizzled by token pairs
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int tok = 16 * (c & 1) + 8 * j + (lane & 7), m = (lane >> 3) ^ ((tok >> 1) & 3);
+                            stmatrix_x4_trans(smem_u32(stage_out + tok * 64 + m * 16), pack_bf16x2(v[0][j][0], v[0][j][1]),
+                                              pack_bf16x2(v[1][j][0], v[1][j][1]), pack_bf16x2(v[2][j][0], v[2][j][1]),
+                                              pack_bf16x2(v[3][j][0], v[3][j][1]));
+                        }
+                        if ((c & 1) == 0 && left > 16 * (c + 1)) continue;
+                        const int n = left - 32 * (c >> 1) < 32 ? left - 32 * (c >> 1) : 32;
+                        TO* out = static_cast<TO*>(p.out) + (int64_t)(t.row0 + 64 * r + 32 * (c >> 1)) * p.ldo + cur.f0;
+                        __syncwarp();
+                        if (live && p.vec_out && cur.f0 + 32 <= p.N) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                const int tok = 8 * s + gl, m = (lane & 3) ^ ((tok >> 1) & 3);
+                                const uint4 w = *reinterpret_cast<const uint4*>(stage_out + tok * 64 + m * 16);
+                                if (tok < n) *reinterpret_cast<uint4*>(out + (int64_t)tok * p.ldo + 8 * (lane & 3)) = w;
+                            }
+                        } else if (live) {
+                            for (int tok = 0; tok < n; ++tok) {
+                                const int m = (lane >> 3) ^ ((tok >> 1) & 3);
+                                const uint16_t w = *reinterpret_cast<const uint16_t*>(stage_out + tok * 64 + m * 16 + 2 * (lane & 7));
+                                if (cur.f0 + lane < p.N) reinterpret_cast<uint16_t*>(out)[(int64_t)tok * p.ldo + lane] = w;
+                            }
+                        }
+                        __syncwarp();  // the chunk is read
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty_l);  // TMEM drained: the next tile's MMAs may start
-            if (kPacked && live) {
-                // for each token the warp writes 32 consecutive features of each accumulator
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    const int n = t.n - 64 * r - 16 * ch;
-                    TO* dst = out + (int64_t)16 * ch * p.ldo;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < n) {
-                            const int sh = (i & 1) * 16;
-                            if (f < p.N) reinterpret_cast<uint16_t*>(dst)[i * p.ldo + f] = (uint16_t)(h1[ch][i >> 1] >> sh);
-                            if (EPI != I8_SWIGLU && f2 < p.N)
-                                reinterpret_cast<uint16_t*>(dst)[i * p.ldo + f2] = (uint16_t)(h2[ch][i >> 1] >> sh);
-                        }
-                }
-            }
+            cur = next;
         }
     }
 
@@ -409,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int EPI, typename TO>
-int launch(const CUtensorMap& mw, const CUtensorMap& mw2, const CUtensorMap& mx, const Params& kp, int grid,
+int launch(const CUtensorMap& mw, const CUtensorMap& mw2, const CUtensorMap& mx, const CUtensorMap& mx128, const Params& kp, int grid,
            cudaStream_t stream) {
     static bool attr_set[64] = {false};
     int dev = 0;
@@ -419,8 +521,7 @@ int launch(const CUtensorMap& mw, const CUtensorMap& mw2, const CUtensorMap& mx,
                                           (int)kSmemBytes));
         if (dev < 64) attr_set[dev] = true;
     }
-    i8_kernel<EPI, TO><<<grid, kThreads, kSmemBytes, stream>>>(mw, mw2, mx, kp);
-    return launch_status();
+    return launch_pdl(i8_kernel<EPI, TO>, grid, kThreads, kSmemBytes, stream, mw, mw2, mx, mx128, kp);
 }
 
 }  // namespace
@@ -447,28 +548,39 @@ int i8_gemm_run(const I8Problem& p, cudaStream_t stream) {
     Params kp{};
     kp.G = p.G, kp.M = p.M, kp.N = p.N, kp.offsets = p.offsets;
     kp.xscale = p.xscale, kp.wscale = p.wscale, kp.wscale2 = p.wscale2, kp.bias = p.bias;
-    kp.tile_f = dual ? 2 * kM : 4 * kM;
+    kp.tile_f = dual ? kM : 2 * kM;
     kp.f_tiles = (int)((p.N + kp.tile_f - 1) / kp.tile_f);
     kp.k_blocks = (int)((p.K + kBK - 1) / kBK);
-    kp.out = p.out, kp.ldo = p.ldo, kp.tile_counter = p.tile_counter, kp.status = p.status;
-    const int64_t max_tiles = kp.f_tiles * ((p.M + kNT - 1) / kNT + p.G - 1);  // every group may end a tile early
+    kp.out = p.out, kp.ldo = p.ldo, kp.status = p.status;
+    kp.vec_out = aligned16(p.out) && (p.ldo * dtype_size(p.out_dtype)) % 16 == 0;
+    // One group: smaller tiles while they leave pairs idle, all of a size, so the pairs take them in turn.  Several:
+    // tiles of up to 256 tokens, drawn from the counter.
+    int64_t pairs = device_sm_count() / 2;
+    kp.max_span = kNT;
+    if (p.G == 1)
+        while (kp.max_span > 2 * kBox && 2 * kp.f_tiles * ((p.M + kp.max_span - 1) / kp.max_span) <= pairs) kp.max_span /= 2;
+    const int64_t max_tiles = kp.f_tiles * ((p.M + kp.max_span - 1) / kp.max_span + p.G - 1);  // every group may end one early
     MOE_REQUIRE(max_tiles < (int64_t(1) << 30), MOE_ERR_UNSUPPORTED);
 
-    CUtensorMap mw, mw2, mx;
-    MOE_REQUIRE(make_map_i8(&mw, p.w, p.K, p.G * p.N, p.ldw, kM), MOE_ERR_CUDA);
-    MOE_REQUIRE(make_map_i8(&mw2, dual ? p.w2 : p.w, p.K, p.G * p.N, p.ldw, kM), MOE_ERR_CUDA);
+    CUtensorMap mw, mw2, mx, mx128;
+    MOE_REQUIRE(make_map_i8(&mw, p.w, p.K, p.G * p.N, p.ldw, dual ? kM / 2 : kM), MOE_ERR_CUDA);
+    if (dual) MOE_REQUIRE(make_map_i8(&mw2, p.w2, p.K, p.G * p.N, p.ldw, kM / 2), MOE_ERR_CUDA);
+    else mw2 = mw;
     MOE_REQUIRE(make_map_i8(&mx, p.x, p.K, p.M, p.ldx, kBox), MOE_ERR_CUDA);
-    MOE_CUDA_TRY(cudaMemsetAsync(p.tile_counter, 0, sizeof(uint32_t), stream));
-    int64_t pairs = device_sm_count() / 2;
+    MOE_REQUIRE(make_map_i8(&mx128, p.x, p.K, p.M, p.ldx, kNT / 2), MOE_ERR_CUDA);
+    if (p.G > 1 && max_tiles > pairs) {
+        kp.tile_counter = p.tile_counter;
+        MOE_CUDA_TRY(cudaMemsetAsync(p.tile_counter, 0, sizeof(uint32_t), stream));
+    }
     if (max_tiles < pairs) pairs = max_tiles;
     if (pairs < 1) pairs = 1;
     const int grid = (int)(2 * pairs);
     const bool bf = p.out_dtype == MOE_BF16;
     switch (p.epilogue) {
-        case I8_OUT: return bf ? launch<I8_OUT, __nv_bfloat16>(mw, mw2, mx, kp, grid, stream)
-                               : launch<I8_OUT, float>(mw, mw2, mx, kp, grid, stream);
-        case I8_GELU: return bf ? MOE_ERR_UNSUPPORTED : launch<I8_GELU, float>(mw, mw2, mx, kp, grid, stream);
-        case I8_SWIGLU: return bf ? MOE_ERR_UNSUPPORTED : launch<I8_SWIGLU, float>(mw, mw2, mx, kp, grid, stream);
+        case I8_OUT: return bf ? launch<I8_OUT, __nv_bfloat16>(mw, mw2, mx, mx128, kp, grid, stream)
+                               : launch<I8_OUT, float>(mw, mw2, mx, mx128, kp, grid, stream);
+        case I8_GELU: return bf ? MOE_ERR_UNSUPPORTED : launch<I8_GELU, float>(mw, mw2, mx, mx128, kp, grid, stream);
+        case I8_SWIGLU: return bf ? MOE_ERR_UNSUPPORTED : launch<I8_SWIGLU, float>(mw, mw2, mx, mx128, kp, grid, stream);
         default: return MOE_ERR_INVALID_ARG;
     }
 }

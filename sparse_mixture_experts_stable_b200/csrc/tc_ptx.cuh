@@ -146,6 +146,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// The same without release semantics, for a thread that has nothing to publish: a release waits for all of the
+// thread's global stores first, thousands of cycles after an epilogue's.  `after` is a value that the thread has read
+// before it arrives.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster, uint32_t after) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];  // after %1" ::"r"(bar_cluster), "r"(after)
+                 : "memory");
+}
+
 // TMA tile load into this CTA's shared memory whose completion is counted on an
 // mbarrier of either CTA of the pair (shared::cluster address); no multicast.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
@@ -324,6 +332,15 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                   "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
+                   "+r"(a[15])
+                 :
+                 : "memory");
+}
+
 // 16 consecutive fp32 columns of this thread's TMEM lane, and the matching wait.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -342,6 +359,25 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[16], uint32_t (&b)[16
                    "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]),
                    "+r"(b[14]), "+r"(b[15])
                  :
+                 : "memory");
+}
+
+// 32 TMEM lanes x 16 columns.  Register 8 h + 4 j + i of lane l: row 16 h + l / 4 (+ 8 for i >= 2), column
+// 8 j + 2 (l % 4) + i % 2.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr + (16u << 16)));
+}
+
+// Four 8 x 8 matrices of 16-bit values (lane l: row l / 4, columns 2 (l % 4) and the next), each written transposed:
+// lanes 8 m .. 8 m + 7 give the addresses of the 16-byte rows that matrix m's columns become.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
                  : "memory");
 }
 
