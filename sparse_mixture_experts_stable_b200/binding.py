@@ -818,8 +818,10 @@ def _out(o: dict, name: str, shape, dtype, dev):
 
 def _padded(rows_shape, K: int, dev) -> torch.Tensor:
     """int8 (*rows_shape, K) whose rows start on multiples of 16 bytes."""
-    q = torch.empty(*rows_shape, -(-K // 16) * 16, dtype=torch.int8, device=dev)
-    return q if K % 16 == 0 else q[..., :K]
+    strides = [1, -(-K // 16) * 16]
+    for n in reversed(rows_shape[1:]):
+        strides.append(strides[-1] * n)
+    return torch.empty_strided((*rows_shape, K), strides[::-1], dtype=torch.int8, device=dev)
 
 
 def moe_sort_workspace_size(T: int, k: int, E: int) -> int:

@@ -236,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint8_t* st = smem + stage * kStageBytes;
                     tma_load_2d_pair(st, &tmW, kb * kBK, w_y, fb);
                     if (EPI == I8_SWIGLU) tma_load_2d_pair(st + kWBytes / 2, &tmW2, kb * kBK, w_y, fb);
-                    if (nbox == 4)
+                    if (nbox == 4)  // most often: one copy is issued faster than four
                         tma_load_2d_pair(st + kWBytes, &tmX128, kb * kBK, x_y, fb);
                     else
                         for (int b = 0; b < nbox; ++b)
@@ -543,7 +543,7 @@ int i8_gemm_run(const I8Problem& p, cudaStream_t stream) {
     MOE_REQUIRE(!dual || aligned16(p.w2), MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE((reinterpret_cast<uintptr_t>(p.out) % dtype_size(p.out_dtype)) == 0, MOE_ERR_INVALID_ARG);
     if (i8_skinny_fits(p.M, p.G, p.N, p.K)) return i8_skinny_run(p, false, stream);
-    MOE_REQUIRE(p.tile_counter, MOE_ERR_WORKSPACE);
+    MOE_REQUIRE(p.G == 1 || p.tile_counter, MOE_ERR_WORKSPACE);
 
     Params kp{};
     kp.G = p.G, kp.M = p.M, kp.N = p.N, kp.offsets = p.offsets;
@@ -567,7 +567,8 @@ int i8_gemm_run(const I8Problem& p, cudaStream_t stream) {
     if (dual) MOE_REQUIRE(make_map_i8(&mw2, p.w2, p.K, p.G * p.N, p.ldw, kM / 2), MOE_ERR_CUDA);
     else mw2 = mw;
     MOE_REQUIRE(make_map_i8(&mx, p.x, p.K, p.M, p.ldx, kBox), MOE_ERR_CUDA);
-    MOE_REQUIRE(make_map_i8(&mx128, p.x, p.K, p.M, p.ldx, kNT / 2), MOE_ERR_CUDA);
+    if (kp.max_span == kNT) MOE_REQUIRE(make_map_i8(&mx128, p.x, p.K, p.M, p.ldx, kNT / 2), MOE_ERR_CUDA);
+    else mx128 = mx;
     if (p.G > 1 && max_tiles > pairs) {
         kp.tile_counter = p.tile_counter;
         MOE_CUDA_TRY(cudaMemsetAsync(p.tile_counter, 0, sizeof(uint32_t), stream));
@@ -603,7 +604,7 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 }  // namespace
 
 extern "C" size_t moe_matmul_i8_workspace_size(int64_t M, int32_t G, int64_t N, int64_t K) {
-    return M < 1 || G < 1 || N < 1 || K < 1 || i8_skinny_fits(M, G, N, K) ? 0 : kCounterBytes;
+    return M < 1 || G <= 1 || N < 1 || K < 1 || i8_skinny_fits(M, G, N, K) ? 0 : kCounterBytes;
 }
 
 extern "C" int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, int64_t ldx, const int32_t* offsets,
