@@ -68,7 +68,7 @@ typedef enum {
     MOE_ERR_UNSUPPORTED = 2, /* valid per the pages but outside this build's limits */
     MOE_ERR_CUDA = 3,        /* a CUDA runtime or driver call failed */
     MOE_ERR_BAD_INDEX = 4,   /* device: an expert index outside [0, E) */
-    MOE_ERR_NONFINITE = 5,   /* device: a non-finite router logit */
+    MOE_ERR_NONFINITE = 5,   /* device: a non-finite router logit, or value to quantise */
     MOE_ERR_TIMEOUT = 6,     /* device: a bounded wait gave up */
     MOE_ERR_WORKSPACE = 7    /* workspace NULL or smaller than required */
 } moe_status;
@@ -520,7 +520,7 @@ MOE_API int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, int6
  *   SWIGLU   : q(silu(X W1^T) * (X W3^T)) W2^T                w1 = gate, w3 = up (G, F, D), w2 = down (G, Dout, F)   [P3]
  * q: the rows of the hidden activation, kept in fp32 until then, quantised as
  * moe_quantize_i8 does.  Row strides ldw1 (w1 and w3) and ldw2; biases fp32 or
- * NULL; ys device (M, Dout), row stride ldys, `out_dtype`; offsets, limits,
+ * NULL (NULL for SWIGLU); ys device (M, Dout), row stride ldys, `out_dtype`; offsets, limits,
  * alignment, rows outside the groups and the status word as moe_matmul_i8.
  *   workspace >= moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout)
  *   bytes on a 16-byte boundary, one per call in flight.

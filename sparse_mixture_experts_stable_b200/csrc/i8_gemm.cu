@@ -638,6 +638,7 @@ extern "C" int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const floa
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     MOE_REQUIRE(kind == MOE_FFN_LINEAR || kind == MOE_FFN_GELU_MLP || kind == MOE_FFN_SWIGLU, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(ffn_sizes_ok(kind, G, M, D, F, Dout), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(kind != MOE_FFN_SWIGLU || (!b1 && !b2), MOE_ERR_INVALID_ARG);
     if (M == 0) return MOE_OK;
     MOE_REQUIRE(workspace && workspace_bytes >= moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout),
                 MOE_ERR_WORKSPACE);

@@ -109,6 +109,89 @@ class SwiGLUMoE:
         return dict(y=self.y, f=f, P=P, aux=aux, **r, **d)
 
 
+class SwiGLUMoEInt8:
+    """SwiGLUMoE for serving, without a capacity and with its experts in 8 bits.
+
+    y = shared(x) + sum_j gate_j * Expert_{e_j}(x), nothing dropped.  The tokens are quantised as they are sorted by
+    expert, the hidden rows between the two products, both with one scale per row; the weights have one per output channel.
+    """
+
+    def __init__(self, T: int, H: int, E: int, F: int, k: int, F_shared: int = 0, aux_coef: float = 0.0,
+                 dtype=torch.bfloat16, device="cuda"):
+        self.T, self.H, self.E, self.F, self.k = T, H, E, F, k
+        self.F_shared, self.aux_coef, self.dtype = F_shared, aux_coef, dtype
+        dev = torch.device(device)
+        dt = B.MOE_BF16 if dtype == torch.bfloat16 else B.MOE_F32
+        self.route_out = dict(
+            selected=torch.empty(T, k, dtype=torch.int64, device=dev),
+            gates=torch.empty(T, k, dtype=dtype, device=dev),
+            gates_f32=torch.empty(T, k, dtype=torch.float32, device=dev),
+            counts=torch.empty(E, dtype=torch.int32, device=dev),
+            prob_sum=torch.empty(E, dtype=torch.float32, device=dev),
+        )
+        pad = -(-H // 16) * 16
+        self.sort_out = dict(
+            offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+            row=torch.empty(T, k, dtype=torch.int32, device=dev),
+            source=torch.empty(T * k, dtype=torch.int32, device=dev),
+            xq=torch.empty(T * k, pad, dtype=torch.int8, device=dev)[:, :H],
+            xscale=torch.empty(T * k, dtype=torch.float32, device=dev),
+        )
+        self.ys = torch.empty(T * k, H, dtype=dtype, device=dev)
+        self.y = torch.empty(T, H, dtype=dtype, device=dev)
+        self.status = B.new_status(dev)
+        self.ws_route = torch.empty(max(B.moe_route_workspace_size(T, H, E, dt, True, "ED"), 256),
+                                    dtype=torch.uint8, device=dev)
+        self.ws_sort = torch.empty(max(B.moe_sort_workspace_size(T, k, E), 256), dtype=torch.uint8, device=dev)
+        self.ws_ffn = torch.empty(max(B.moe_expert_ffn_i8_workspace_size("swiglu", E, T * k, H, F, H), 256),
+                                  dtype=torch.uint8, device=dev)
+        if F_shared:
+            self.xq = torch.empty(T, pad, dtype=torch.int8, device=dev)[:, :H]
+            self.xscale = torch.empty(T, dtype=torch.float32, device=dev)
+            self.shared = torch.empty(T, H, dtype=dtype, device=dev)
+            self.ws_shared = torch.empty(max(B.moe_expert_ffn_i8_workspace_size("swiglu", 1, T, H, F_shared, H), 256),
+                                         dtype=torch.uint8, device=dev)
+        self.side = None  # stream for the shared expert, created on first use
+
+    @staticmethod
+    def quantize(w_gate, w_up, w_down) -> dict:
+        """Expert weights (E,F,H), (E,F,H) and (E,H,F) in 8 bits, as ``forward`` takes them."""
+        q = {}
+        for name, w in (("1", w_gate), ("3", w_up), ("2", w_down)):
+            q["w" + name], q["s" + name] = B.moe_quantize_i8(w)
+        return q
+
+    def forward(self, x, w_router, router_bias, experts, shared=None):
+        """x (T,H); w_router (E,H); ``experts`` and ``shared`` (the latter with E = 1) from ``quantize``.
+
+        The shared expert runs on a second stream, as in SwiGLUMoE.
+        """
+        main = torch.cuda.current_stream(x.device)
+        base = None
+        if self.F_shared:
+            if self.side is None:
+                self.side = torch.cuda.Stream(device=x.device)
+                self.ev_x, self.ev_shared = torch.cuda.Event(), torch.cuda.Event()
+            self.ev_x.record(main)
+            self.side.wait_event(self.ev_x)
+            B.moe_quantize_i8(x, q=self.xq, scale=self.xscale, dev_status=self.status, stream=self.side)
+            B.moe_expert_ffn_i8("swiglu", self.xq, self.xscale, None, ys=self.shared, dev_status=self.status,
+                                workspace=self.ws_shared, stream=self.side, **shared)
+            self.ev_shared.record(self.side)
+            base = self.shared
+        r = B.moe_route(x, self.k, w_router=w_router, layout="ED", logit_bias=router_bias, out=self.route_out,
+                        dev_status=self.status, workspace=self.ws_route)
+        d = B.moe_sort_i8(r["selected"], self.E, x, out=self.sort_out, dev_status=self.status, workspace=self.ws_sort)
+        B.moe_expert_ffn_i8("swiglu", d["xq"], d["xscale"], d["offsets"], ys=self.ys, dev_status=self.status,
+                            workspace=self.ws_ffn, **experts)
+        if self.F_shared:
+            main.wait_event(self.ev_shared)
+        B.moe_unsort(self.ys, d["row"], r["gates_f32"], base=base, y=self.y, dev_status=self.status)
+        f, P, aux = B.moe_aux_stats(r["counts"], r["prob_sum"], self.T, self.k, True, self.aux_coef,
+                                    out_dtype=self.dtype)
+        return dict(y=self.y, f=f, P=P, aux=aux, **r, **d)
+
+
 class SwiGLULayer:
     """The same layer as SwiGLUMoE through the single C call moe_swiglu_layer_forward.
 
