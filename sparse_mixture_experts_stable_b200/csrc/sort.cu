@@ -439,7 +439,7 @@ int sort_run(SortParams p, int op, moe_dtype dtype, void* workspace, size_t work
 
 // ------------------------------- and back -----------------------------------
 
-// V: 16 bytes, or one element, of a row of T; its values as fp32
+// V: 16 or 4 bytes, or one value, of a row of T; its values as fp32
 template <typename T, typename V>
 struct Vec {
     static constexpr int kN = sizeof(V) / sizeof(T);
@@ -574,31 +574,30 @@ __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) 
     }
 }
 
-// dys[row] = gate dy[t] and dgates[t, j] = dy[t] . ys[row], one warp per (t, j).  The warps of a token sit in one
-// block, so that dy's row comes from memory once and from the first-level cache after that.
-template <typename T, typename G, typename V, int U, bool DYS, bool DGATES>
+// dys[row] = gate dy[t] and dgates[t, j] = dy[t] . ys[row], one assignment (t, j) per TEAM lanes.  Those of a token
+// sit in one block, so that dy's row comes from memory once and from the first-level cache after that.
+template <typename T, typename G, typename V, int U, int TEAM, bool DYS, bool DGATES>
 __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const UnsortParams p) {
     constexpr int N = Vec<T, V>::kN;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int at = threadIdx.x % TEAM;
+    const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / TEAM;
     pdl_wait();
     pdl_next();
-    if (unit >= p.T * p.k) return;
-    const int64_t t = unit / p.k;
-    const int64_t r = p.row[unit];
+    const bool mine = unit < p.T * p.k;
+    const int64_t r = mine ? p.row[unit] : -1;
     float dot = 0.f;
     if (r >= 0 && r < p.rows) {
         const float g = p.gates ? to_f32(static_cast<const G*>(p.gates)[unit]) : 1.f;
-        const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
+        const T* dy = static_cast<const T*>(p.dy) + unit / p.k * p.lddy;
         const T* ys = static_cast<const T*>(p.ys) + r * p.ldys;
         T* dys = static_cast<T*>(p.y) + r * p.ldy;
-        for (int64_t c0 = 0; c0 < p.N; c0 += 32 * N * U) {
+        for (int64_t c0 = 0; c0 < p.N; c0 += TEAM * N * U) {
             V a[U], b[U];
             int64_t col[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t c = c0 + 32 * N * u + lane * N;
-                col[u] = c < p.N ? c : p.N - N;
+                const int64_t c = c0 + (TEAM * u + at) * N;
+                col[u] = c < p.N ? c : p.N - N;  // past the end: the last vector again, not used
                 a[u] = *reinterpret_cast<const V*>(dy + col[u]);
                 if (DGATES) b[u] = *reinterpret_cast<const V*>(ys + col[u]);
             }
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const UnsortP
             for (int u = 0; u < U; ++u) {
                 float d[N];
                 Vec<T, V>::unpack(a[u], d);
-                const bool in = c0 + 32 * N * u + lane * N < p.N;
+                const bool in = c0 + (TEAM * u + at) * N < p.N;
                 if (DGATES) {
                     float v[N];
                     Vec<T, V>::unpack(b[u], v);
@@ -622,12 +621,13 @@ __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const UnsortP
                 }
             }
         }
-    } else if (r != -1 && lane == 0) {
+    } else if (mine && r != -1 && at == 0) {
         set_status(p.status, MOE_ERR_BAD_INDEX);
     }
     if (DGATES) {
-        dot = warp_sum(dot);
-        if (lane == 0) p.dgates[unit] = dot;
+#pragma unroll
+        for (int o = TEAM / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (mine && at == 0) p.dgates[unit] = dot;
     }
 }
 
@@ -642,21 +642,35 @@ int launch_unsort(UnsortParams p, cudaStream_t stream) {
     return launch_pdl(unsort_kernel<T, G, V, J, U>, grid, kThreads, 0, stream, p);
 }
 
-template <typename T, typename G, typename V, int U>
+template <typename T, typename G, typename V, int U, int TEAM>
 int launch_backward(const UnsortParams& p, cudaStream_t stream) {
-    const int64_t grid = (p.T * p.k + kWarps - 1) / kWarps;
-    if (p.y && p.dgates) return launch_pdl(unsort_backward_kernel<T, G, V, U, true, true>, grid, kThreads, 0, stream, p);
-    if (p.y) return launch_pdl(unsort_backward_kernel<T, G, V, U, true, false>, grid, kThreads, 0, stream, p);
-    return launch_pdl(unsort_backward_kernel<T, G, V, U, false, true>, grid, kThreads, 0, stream, p);
+    const int64_t grid = (p.T * p.k * TEAM + kThreads - 1) / kThreads;
+    const auto go = [&](auto kernel) { return launch_pdl(kernel, grid, kThreads, 0, stream, p); };
+    if (p.y && p.dgates) return go(unsort_backward_kernel<T, G, V, U, TEAM, true, true>);
+    return p.y ? go(unsort_backward_kernel<T, G, V, U, TEAM, true, false>)
+               : go(unsort_backward_kernel<T, G, V, U, TEAM, false, true>);
 }
 
-// Rows that 16 bytes divide, or single elements (two loads for each of the 16-byte form's).
+// V: the widest of 16 bytes, 4 and one value that the rows' starts and length allow.  T = 16384, k = 8 bf16: the way back
+// and its gradient take 118 and 179 us at D = 2048, 146 and 228 at 2046, 296 and 297 at 2047.  (Whole 16-byte loads shifted
+// to an odd row's start took 228 and 449.)  Loads at a time: 8 vectors, for narrower ones 16 on the way back; the gradient
+// 4 of each operand, for fp32 values 8 (D = 1001: 221 us, 263 with 4; bf16 D = 2046: 284 us with 8).
+// The gradient of rows of up to eight vectors: eight lanes each (D = 64: 9 us, 44 with a warp each).
+template <typename T, typename G, typename V, int X>
+int launch_back(const UnsortParams& p, bool backward, cudaStream_t stream) {
+    if (backward)
+        return p.N <= 8 * Vec<T, V>::kN ? launch_backward<T, G, V, 1, 8>(p, stream) : launch_backward<T, G, V, sizeof(T) == 2 ? 4 : 4 * X, 32>(p, stream);
+    if (p.k >= 6) return launch_unsort<T, G, V, 8, X>(p, stream);
+    if (p.k >= 3) return launch_unsort<T, G, V, 4, 2 * X>(p, stream);
+    return launch_unsort<T, G, V, 2, 4 * X>(p, stream);
+}
+
 template <typename T, typename G>
-int launch_back(const UnsortParams& p, bool backward, bool vec, cudaStream_t stream) {
-    if (backward) return vec ? launch_backward<T, G, uint4, 4>(p, stream) : launch_backward<T, G, T, 8>(p, stream);
-    if (p.k >= 6) return vec ? launch_unsort<T, G, uint4, 8, 1>(p, stream) : launch_unsort<T, G, T, 8, 2>(p, stream);
-    if (p.k >= 3) return vec ? launch_unsort<T, G, uint4, 4, 2>(p, stream) : launch_unsort<T, G, T, 4, 4>(p, stream);
-    return vec ? launch_unsort<T, G, uint4, 2, 4>(p, stream) : launch_unsort<T, G, T, 2, 8>(p, stream);
+int launch_back(const UnsortParams& p, bool backward, int bytes, cudaStream_t stream) {
+    if (bytes == 16) return launch_back<T, G, uint4, 1>(p, backward, stream);
+    if constexpr (sizeof(T) == 2)
+        if (bytes < 4) return launch_back<T, G, uint16_t, 2>(p, backward, stream);
+    return launch_back<T, G, uint32_t, 2>(p, backward, stream);
 }
 
 int unsort_run(const UnsortParams& p, bool backward, moe_dtype dtype, moe_dtype gate_dtype, cudaStream_t stream) {
@@ -665,13 +679,13 @@ int unsort_run(const UnsortParams& p, bool backward, moe_dtype dtype, moe_dtype 
                           reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.dy) |
                           (uintptr_t)(p.N * es) | (uintptr_t)(p.ldys * es) | (uintptr_t)(p.ldy * es) |
                           (uintptr_t)(p.ldbase * es) | (uintptr_t)(p.lddy * es);
-    const bool vec = (all & 15) == 0;
+    const int bytes = (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 2;
     const bool gb = gate_dtype == MOE_BF16;
     if (dtype == MOE_BF16)
-        return gb ? launch_back<__nv_bfloat16, __nv_bfloat16>(p, backward, vec, stream)
-                  : launch_back<__nv_bfloat16, float>(p, backward, vec, stream);
-    return gb ? launch_back<float, __nv_bfloat16>(p, backward, vec, stream)
-              : launch_back<float, float>(p, backward, vec, stream);
+        return gb ? launch_back<__nv_bfloat16, __nv_bfloat16>(p, backward, bytes, stream)
+                  : launch_back<__nv_bfloat16, float>(p, backward, bytes, stream);
+    return gb ? launch_back<float, __nv_bfloat16>(p, backward, bytes, stream)
+              : launch_back<float, float>(p, backward, bytes, stream);
 }
 
 }  // namespace
