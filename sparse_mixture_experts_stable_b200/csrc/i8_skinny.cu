@@ -4,18 +4,18 @@
 // without one.
 //
 // A block takes a contiguous run of units; a unit is up to kTok tokens of a group (they lie
-// in shared memory) and a block of features, 16 weight rows per warp (8 of gate and 8 of up
-// for SwiGLU) or, where units are few, per `ksplit` warps that share the depth.  Every warp
-// streams its rows through a ring of its own, kStages stages of 16 x 256 bytes filled by TMA:
-// 128 KB are in flight per SM whatever the arithmetic takes, at two instructions per stage
-// (a bulk copy per row took longer to issue than to arrive), and no warp waits for another
-// one's loads.  Products are m16n8k32 of the warp-level tensor instructions on 8-bit
-// integers: with dp4a the arithmetic of 8 tokens took twice as long as the weights' way from
-// memory, with these it is a tenth of it, so tcgen05 has nothing to win here.  The order of
-// k is free as long as both operands share it, so a lane's four bytes of each fragment are
-// neighbours and come in 16-byte reads.  With fp32 rows (the experts' hidden rows) every
-// block quantises the rows that it stages: a few KB, against a launch and a round trip
-// through memory.
+// in shared memory) and a block of 128 weight rows (64 of gate and 64 of up for SwiGLU), 16
+// per warp; where units are few, `ksplit` warps share 16 rows' depth and a unit has fewer
+// rows.  One thread fills a ring of kStages stages of 32 KB, 256 bytes of each row, by TMA:
+// up to 160 KB are in flight per SM whatever the arithmetic takes.  (Rings of the warps' own
+// took 8 to 16 copies for the same 32 KB; the SM issues one in some 70 cycles, and that was
+// as long as the memory needs.)  256 bytes per row want no swizzle, so the reads of the
+// fragments meet two-way bank conflicts.  Products are m16n8k32 of the warp-level tensor
+// instructions on 8-bit integers: a tenth of the weights' time, so tcgen05 has nothing to
+// win here.  The order of k is free as long as both operands share it, so a lane's four
+// bytes of each fragment are neighbours and come in 16-byte reads.  With fp32 rows (the
+// experts' hidden rows) every block quantises the rows that it stages: a few KB, against a
+// launch and a round trip through memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,17 +29,17 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 16;    // weight rows of a stage
-constexpr int kSeg = 256;    // bytes of each: two TMA boxes side by side
-constexpr int kStageBytes = kRows * kSeg;
+constexpr int kWarps = 8;                      // that multiply; one more loads
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kRows = 16;                      // weight rows of a warp
+constexpr int kSeg = 256;                      // bytes of each in a stage
+constexpr int kStageBytes = kWarps * kRows * kSeg;
 constexpr int kStages = 5;
 constexpr int kTok = 16;                 // tokens in shared memory at a time, at most
 constexpr int kMaxG = 1024;
 constexpr int64_t kMaxK = 4096;
-constexpr size_t kRingBytes = (size_t)kWarps * kStages * kStageBytes;
-constexpr size_t kTokBytes = (size_t)kTok * (2048 + 64);
+constexpr size_t kRingBytes = (size_t)kStages * kStageBytes;
+constexpr size_t kTokBytes = (size_t)kTok * (2048 + 64) + kSeg;  // the last piece is read whole
 
 struct SkinnyParams {
     I8Problem p;
@@ -64,14 +64,14 @@ static __device__ __noinline__ uint4 load_part(const int8_t* s, int n) {
 // d += a b: 16 weight rows x 32 values, 8 tokens
 __device__ __forceinline__ void mma_i8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// the threads of one team of warps
-__device__ __forceinline__ void team_sync(int team, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+// `threads` of the block; barrier 0 is __syncthreads'
+__device__ __forceinline__ void part_sync(int barrier, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
 }
 
 // A place in the sequence of units: item (tokens of a group) and feature block.
@@ -107,28 +107,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_w2,
                   const SkinnyParams sp) {
     constexpr int FROWS = EPI == I8_SWIGLU ? kRows / 2 : kRows;  // output features of 16 weight rows
-    extern __shared__ uint8_t s_raw[];                           // rings of the warps, then the tokens (tok, xpitch)
-    __shared__ uint64_t s_bar[kWarps][kStages];
-    __shared__ int s_prefix[kMaxG + 1], s_off[kMaxG + 1];
+    extern __shared__ uint8_t s_raw[];                           // the ring, then the tokens (tok, xpitch)
+    __shared__ uint64_t s_full[kStages], s_empty[kStages];
+    __shared__ int s_prefix[kMaxG + 1], s_off[kMaxG], s_end[kMaxG];
     __shared__ float s_scale[kTok];
     __shared__ int s_red[2][kWarps][8][32];
-    uint8_t* s_dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 127) & ~uintptr_t(127));
+    uint8_t* s_x = ring + kRingBytes;
     const I8Problem& p = sp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kpart = warp % sp.ksplit, team = warp / sp.ksplit, teams = kWarps / sp.ksplit;
-    uint8_t* ring = s_dyn + (size_t)warp * kStages * kStageBytes;
-    uint8_t* s_x = s_dyn + kRingBytes;
-    if (lane < kStages) tc::mbar_init(&s_bar[warp][lane], 1);
+    const int teams = kWarps / sp.ksplit;
+    if (threadIdx.x < kStages) {
+        tc::mbar_init(&s_full[threadIdx.x], 1);
+        tc::mbar_init(&s_empty[threadIdx.x], kWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
     pdl_next();
-    for (int g = threadIdx.x; g <= p.G; g += kThreads)
-        s_off[g] = p.offsets ? min(max(p.offsets[g], 0), (int)p.M) : g == 0 ? 0 : (int)p.M;
-    __syncthreads();
     for (int g = threadIdx.x; g < p.G; g += kThreads) {
-        const int n = s_off[g + 1] - s_off[g];
-        if (n < 0) set_status(p.status, MOE_ERR_BAD_INDEX);
-        s_prefix[g] = n > 0 ? (n + sp.tok - 1) / sp.tok : 0;
+        int lo = 0, hi = (int)p.M;
+        if (p.offsets) lo = min(max(p.offsets[g], 0), hi), hi = min(max(p.offsets[g + 1], 0), hi);
+        if (hi < lo) set_status(p.status, MOE_ERR_BAD_INDEX);
+        s_off[g] = lo;
+        s_end[g] = hi;
+        s_prefix[g] = hi > lo ? (hi - lo + sp.tok - 1) / sp.tok : 0;
     }
     __syncthreads();
     block_scan<kThreads>(s_prefix, p.G);
@@ -136,48 +138,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
     if (u0 >= u1) return;
 
-    Cursor load, use;
-    load.seek(u0, sp.fblocks, s_prefix, p.G);
-    use = load;
-    int load_unit = u0, load_seg = kpart, ahead = 0;  // ahead: stages on their way
-    // where this warp's features of a unit begin; it takes part if they exist
-    const auto feature = [&](const Cursor& c) { return ((int64_t)c.fb * teams + team) * FROWS; };
-    // Fills the stage with the next piece of this warp's sequence, if there is one.
-    const auto fetch = [&](int stage) {
-        while (load_unit < u1 && (feature(load) >= p.N || load_seg >= sp.segs)) {
-            ++load_unit;
-            load_seg = kpart;
-            load.next(sp.fblocks, s_prefix, p.G);
-        }
-        if (load_unit >= u1) return;
+    Cursor use;
+    use.seek(u0, sp.fblocks, s_prefix, p.G);
+    if (warp == kWarps) {
+        // -------------------------------- loads --------------------------------
         if (lane == 0) {
-            uint64_t* bar = &s_bar[warp][stage];
-            uint8_t* dst = ring + stage * kStageBytes;
-            const int row = (int)(load.g * p.N + feature(load));
-            tc::mbar_expect_tx(bar, kStageBytes);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int k = load_seg * kSeg + b * 128;
-                tc::tma_load_2d(dst + b * kRows * 128, &tm_w, k, row, bar);
-                if (EPI == I8_SWIGLU) tc::tma_load_2d(dst + b * kRows * 128 + FROWS * 128, &tm_w2, k, row, bar);
+            const int rows = teams * kRows, half = teams * FROWS;  // of a piece of the depth; of gate, for SwiGLU
+            int stage = 0;
+            uint32_t phase = 0, used = 0, last = 0;  // used, last: a bit per stage
+            bool ok = true;
+            for (int unit = u0; unit < u1 && ok; ++unit, use.next(sp.fblocks, s_prefix, p.G)) {
+                const int row = (int)(use.g * p.N + (int64_t)use.fb * half);
+                for (int seg = 0; seg < sp.segs; seg += sp.ksplit) {
+                    if (!tc::mbar_wait(&s_empty[stage], phase ^ 1u, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const int parts = min(sp.ksplit, sp.segs - seg);
+                    uint8_t* dst = ring + stage * kStageBytes;
+                    tc::mbar_expect_tx(&s_full[stage], (uint32_t)(parts * rows * kSeg));
+                    for (int k = 0; k < parts; ++k, dst += rows * kSeg) {
+                        tc::tma_load_2d(dst, &tm_w, (seg + k) * kSeg, row, &s_full[stage]);
+                        if (EPI == I8_SWIGLU) tc::tma_load_2d(dst + half * kSeg, &tm_w2, (seg + k) * kSeg, row, &s_full[stage]);
+                    }
+                    used |= 1u << stage;
+                    last = (last & ~(1u << stage)) | phase << stage;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
             }
+            for (int s = 0; s < kStages; ++s)  // whatever happens, the block does not end before its copies have landed
+                if (used >> s & 1) tc::mbar_wait(&s_full[s], last >> s & 1, p.status);
         }
-        load_seg += sp.ksplit;
-        ++ahead;
-    };
-    for (int s = 0; s < kStages - 1; ++s) fetch(s);
+        return;
+    }
 
-    // Fragment row (weight row, token) and 16-byte column of this lane.  Weight row gl of the fragment is row wr of the
-    // stage, so that the eight lanes of a read see rows 4 apart: the swizzle then gives them different banks.
-    const int gl = lane >> 2, q = lane & 3, wr = gl >> 1 | (gl & 1) << 2;
-    uint32_t phase = 0;                      // a bit per stage
+    // -------------------------------- products --------------------------------
+    const int kpart = warp % sp.ksplit, team = warp / sp.ksplit;
+    // this warp's place in a stage: its piece of the depth, its rows (for SwiGLU those of gate; up's follow all of gate's)
+    const int w_at = kpart * teams * kRows * kSeg + team * FROWS * kSeg, w_second = EPI == I8_SWIGLU ? teams * FROWS * kSeg : 8 * kSeg;
+    bool dead = false;  // a wait timed out (status set): nothing more is written, the barriers are kept
+    const int gl = lane >> 2, q = lane & 3;  // fragment row (weight row, token) and 16-byte column of this lane
+    uint32_t phase = 0;
     int stage = 0, item = -1, t0 = 0, nt = 0;
     for (int unit = u0; unit < u1; ++unit) {
         if (use.item != item) {  // other tokens (the same for all warps)
             item = use.item;
             t0 = s_off[use.g] + (item - s_prefix[use.g]) * sp.tok;
-            nt = min(s_off[use.g + 1] - t0, sp.tok);
-            __syncthreads();  // the tokens before have been read
+            nt = min(s_end[use.g] - t0, sp.tok);
+            part_sync(kWarps + 1, kWarps * 32);  // the tokens before have been read
             if constexpr (F32X) {
                 for (int t = warp; t < nt; t += kWarps) {
                     const float* src = reinterpret_cast<const float*>(p.x) + (int64_t)(t0 + t) * p.ldx;
@@ -194,23 +205,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) s_scale[t] = r.scale;
                 }
             } else {
-                for (int t = warp; t < nt; t += kWarps) {
-                    const int8_t* src = p.x + (int64_t)(t0 + t) * p.ldx;
-                    for (int c = lane * 16; c < sp.xpitch - 64; c += 512) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (c + 16 <= p.K) v = *reinterpret_cast<const uint4*>(src + c);
-                        else if (c < p.K) v = load_part(src + c, (int)p.K - c);
-                        *reinterpret_cast<uint4*>(s_x + t * sp.xpitch + c) = v;
+                // pieces of all tokens, four per thread on their way
+                const int per = (sp.xpitch - 64) / 16;
+                for (int i0 = threadIdx.x; i0 < nt * per; i0 += 4 * kWarps * 32) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int i = i0 + u * kWarps * 32, t = i / per, c = (i - t * per) * 16;
+                        v[u] = make_uint4(0, 0, 0, 0);
+                        if (i >= nt * per) continue;
+                        const int8_t* src = p.x + (int64_t)(t0 + t) * p.ldx + c;
+                        if (c + 16 <= p.K) v[u] = *reinterpret_cast<const uint4*>(src);
+                        else if (c < p.K) v[u] = load_part(src, (int)p.K - c);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int i = i0 + u * kWarps * 32, t = i / per, c = (i - t * per) * 16;
+                        if (i < nt * per) *reinterpret_cast<uint4*>(s_x + t * sp.xpitch + c) = v[u];
                     }
                 }
                 if (threadIdx.x < nt) s_scale[threadIdx.x] = p.xscale[t0 + threadIdx.x];
             }
-            __syncthreads();
+            part_sync(kWarps + 1, kWarps * 32);
         }
-        const int64_t f0 = feature(use);
-        const bool live = f0 < p.N;
-        // features of this lane's sums: weight rows wr and wr + 8
-        const int64_t fa = f0 + wr, fc = EPI == I8_SWIGLU ? fa : fa + 8;
+        const int64_t f0 = ((int64_t)use.fb * teams + team) * FROWS;
+        // features of this lane's sums: weight rows gl and gl + 8
+        const int64_t fa = f0 + gl, fc = EPI == I8_SWIGLU ? fa : fa + 8;
         float wsa = 0.f, wsc = 0.f, ba = 0.f, bc = 0.f;
         if (fa < p.N) wsa = p.wscale[use.g * p.N + fa];
         if (fc < p.N) wsc = (EPI == I8_SWIGLU ? p.wscale2 : p.wscale)[use.g * p.N + fc];
@@ -219,39 +239,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fc < p.N) bc = p.bias[use.g * p.N + fc];
         }
         int acc[2][4] = {}, part[2][4] = {};  // two chains of products each
-        if (live) {
-            for (int seg = kpart; seg < sp.segs; seg += sp.ksplit) {
-                fetch(stage == 0 ? kStages - 1 : stage - 1);
-                const bool landed = __all_sync(0xffffffffu, tc::mbar_wait(&s_bar[warp][stage], phase >> stage & 1, p.status));
-                phase ^= 1u << stage;
-                --ahead;
-                if (!landed) {  // timed out (status set): the copies in flight are waited for, nothing more is written
-                    for (int i = 0; i < ahead; ++i) {
-                        stage = stage + 1 == kStages ? 0 : stage + 1;
-                        tc::mbar_wait(&s_bar[warp][stage], phase >> stage & 1, p.status);
-                    }
-                    return;
-                }
-                const uint8_t* st = ring + stage * kStageBytes + wr * 128;
+        for (int seg = kpart; seg - kpart < sp.segs; seg += sp.ksplit) {
+            if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(&s_full[stage], phase, p.status));
+            if (seg < sp.segs) {
+                const uint8_t* wr = ring + stage * kStageBytes + w_at + gl * kSeg + q * 16;
                 const uint8_t* xr = s_x + gl * sp.xpitch + seg * kSeg + q * 16;
-                const int windows = min(kSeg, (int)p.K - seg * kSeg + 63) / 64;
+                // beyond K the weights' pieces hold zeros
+                uint4 a[kSeg / 64], c[kSeg / 64], b[kSeg / 64];
 #pragma unroll
                 for (int i = 0; i < kSeg / 64; ++i) {
-                    if (i >= windows) break;
-                    const uint8_t* w = st + (i >> 1) * (kRows * 128) + ((4 * (i & 1) + q) ^ wr) * 16;
-                    const uint4 a = *reinterpret_cast<const uint4*>(w);
-                    const uint4 c = *reinterpret_cast<const uint4*>(w + 8 * 128);
-                    const uint4 b = *reinterpret_cast<const uint4*>(xr + 64 * i);
-                    mma_i8(acc[0], a.x, c.x, a.y, c.y, b.x, b.y);
-                    mma_i8(part[0], a.z, c.z, a.w, c.w, b.z, b.w);
-                    if (nt > 8) {
-                        const uint4 d = *reinterpret_cast<const uint4*>(xr + 8 * sp.xpitch + 64 * i);
-                        mma_i8(acc[1], a.x, c.x, a.y, c.y, d.x, d.y);
-                        mma_i8(part[1], a.z, c.z, a.w, c.w, d.z, d.w);
+                    a[i] = *reinterpret_cast<const uint4*>(wr + 64 * i);
+                    c[i] = *reinterpret_cast<const uint4*>(wr + w_second + 64 * i);
+                    b[i] = *reinterpret_cast<const uint4*>(xr + 64 * i);
+                }
+#pragma unroll
+                for (int i = 0; i < kSeg / 64; ++i) {
+                    mma_i8(acc[0], a[i].x, c[i].x, a[i].y, c[i].y, b[i].x, b[i].y);
+                    mma_i8(part[0], a[i].z, c[i].z, a[i].w, c[i].w, b[i].z, b[i].w);
+                }
+                if (nt > 8) {
+#pragma unroll
+                    for (int i = 0; i < kSeg / 64; ++i) b[i] = *reinterpret_cast<const uint4*>(xr + 8 * sp.xpitch + 64 * i);
+#pragma unroll
+                    for (int i = 0; i < kSeg / 64; ++i) {
+                        mma_i8(acc[1], a[i].x, c[i].x, a[i].y, c[i].y, b[i].x, b[i].y);
+                        mma_i8(part[1], a[i].z, c[i].z, a[i].w, c[i].w, b[i].z, b[i].w);
                     }
                 }
-                __syncwarp();  // the stage may be filled again
-                if (++stage == kStages) stage = 0;
+            }
+            __syncwarp();  // the stage is read
+            if (lane == 0) tc::mbar_arrive(&s_empty[stage]);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
 #pragma unroll
@@ -260,13 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sp.ksplit > 1) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) red[warp][i][lane] = acc[i >> 2][i & 3];
-            team_sync(team, 32 * sp.ksplit);
+            part_sync(1 + team, 32 * sp.ksplit);
         }
         // tokens 2q, 2q + 1, 8 + 2q, 9 + 2q; the warps that share the depth share them
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = (i >> 1) * 8 + 2 * q + (i & 1);
-            if (!live || i % sp.ksplit != kpart || (i >> 1) * 8 >= nt) continue;
+            if (dead || f0 >= p.N || i % sp.ksplit != kpart || (i >> 1) * 8 >= nt) continue;
             int sa = acc[i >> 1][i & 1], sc = acc[i >> 1][2 + (i & 1)];
             if (sp.ksplit > 1) {
                 sa = sc = 0;
@@ -300,7 +320,7 @@ int launch(const I8Problem& p, cudaStream_t stream) {
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !attr_set[dev]) {
         MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)(1024 + kRingBytes + kTokBytes)));
+                                          (int)(128 + kRingBytes + kTokBytes)));
         if (dev < 64) attr_set[dev] = true;
     }
     SkinnyParams sp{};
@@ -310,7 +330,7 @@ int launch(const I8Problem& p, cudaStream_t stream) {
     sp.xpitch = (int)((p.K + 127) / 128 * 128 + 64);
     sp.tok = p.K <= 2048 ? kTok : kTok / 2;
     sp.vecx = aligned16(p.x) && p.ldx % 4 == 0;
-    // warps share a row's depth until the blocks have some four units each (more warps on a depth mean more waiting for one another)
+    // warps share a row's depth until the blocks have some two units each (more warps on a depth mean more waiting for one another)
     const int64_t items = (p.M + sp.tok - 1) / sp.tok + (p.M < p.G ? p.M : p.G) - 1;  // at most
     const int64_t sms = device_sm_count();
     int64_t units = 0;
@@ -318,13 +338,14 @@ int launch(const I8Problem& p, cudaStream_t stream) {
         const int64_t per = kWarps / sp.ksplit * (EPI == I8_SWIGLU ? kRows / 2 : kRows);
         sp.fblocks = (int)((p.N + per - 1) / per);
         units = items * sp.fblocks;
-        if (sp.ksplit == kWarps || 2 * sp.ksplit > sp.segs || units >= 4 * sms) break;
+        if (sp.ksplit == kWarps || 2 * sp.ksplit > sp.segs || units >= 2 * sms) break;
     }
     CUtensorMap mw, mw2;
     constexpr bool dual = EPI == I8_SWIGLU;
-    MOE_REQUIRE(make_map_i8(&mw, p.w, p.K, p.G * p.N, p.ldw, dual ? kRows / 2 : kRows), MOE_ERR_CUDA);
-    if (dual) MOE_REQUIRE(make_map_i8(&mw2, p.w2, p.K, p.G * p.N, p.ldw, kRows / 2), MOE_ERR_CUDA);
-    return launch_pdl(kernel, units < sms ? units : sms, kThreads, 1024 + kRingBytes + (size_t)sp.tok * sp.xpitch, stream,
+    const int box = kWarps / sp.ksplit * (dual ? kRows / 2 : kRows);
+    MOE_REQUIRE(make_map_i8(&mw, p.w, p.K, p.G * p.N, p.ldw, box, true), MOE_ERR_CUDA);
+    if (dual) MOE_REQUIRE(make_map_i8(&mw2, p.w2, p.K, p.G * p.N, p.ldw, box, true), MOE_ERR_CUDA);
+    return launch_pdl(kernel, units < sms ? units : sms, kThreads, 128 + kRingBytes + (size_t)sp.tok * sp.xpitch + kSeg, stream,
                       mw, dual ? mw2 : mw, sp);
 }
 
