@@ -421,7 +421,7 @@ MOE_API int moe_combine(const void* ybuf, const int64_t* selected, const int64_t
  *   x         device (T, D), row stride ldx, dtype `dtype`; NULL: the order only.
  *   offsets int32 (E + 1); row int32 (T, k); source int32 (T k): device outputs.
  *   xs        device (T k, D), row stride ldxs, dtype `dtype`.
- *   workspace device, >= moe_sort_workspace_size(T, k, E) bytes (which may be 0).
+ *   workspace device, >= moe_sort_workspace_size(T, k, E) bytes (which may be 0) on a 16-byte boundary.
  */
 MOE_API size_t moe_sort_workspace_size(int64_t T, int32_t k, int32_t E);
 MOE_API int moe_sort(const int64_t* selected, int64_t T, int32_t k, int32_t E, const void* x, moe_dtype dtype,
@@ -491,16 +491,18 @@ MOE_API int moe_quantize_i8(const void* x, moe_dtype dtype, int64_t M, int64_t K
  * moe_matmul_i8 -- product of 8-bit integers with a scale per token and per
  * output channel, dense or grouped over experts:
  *   out[m,n] = (sum_k xq[m,k] wq[g,n,k]) * xscale[m] * wscale[g,n] (+ bias[g,n])   for offsets[g] <= m < offsets[g+1]
- * The sum is an exact int32 on the tensor cores, scaled in fp32 and rounded
- * once.  Rows outside [offsets[0], offsets[G]) are not written.
+ * The sum is an exact int32 on the tensor cores, scaled in fp32 (by wscale
+ * first) and rounded once.  Rows outside [offsets[0], offsets[G]) are not written.
  *   xq        device int8 (M, K), row stride ldx; xscale fp32 (M).
  *   offsets   device int32 (G + 1), ascending, within [0, M] (values outside
- *             are clamped; a group that runs backwards is empty and sets
- *             MOE_ERR_BAD_INDEX), or NULL: G = 1 and all M rows.
+ *             are clamped; where they run backwards the largest so far counts,
+ *             which leaves groups empty, and MOE_ERR_BAD_INDEX is set), or
+ *             NULL: G = 1 and all M rows.
  *   wq        device int8 (G, N, K), row stride ldw (groups N ldw apart); wscale fp32 (G, N).
  *   bias      device fp32 (G, N) or NULL.
  *   out       device (M, N), row stride ldo, `out_dtype`.
- *   workspace device, >= moe_matmul_i8_workspace_size(M, G, N, K) bytes (which may be 0), one per call in flight.
+ *   workspace device, >= moe_matmul_i8_workspace_size(M, G, N, K) bytes (which may be 0) on a
+ *             16-byte boundary, one per call in flight.
  * xq and wq start on 16 bytes with row strides of multiples of 16 (K itself is
  * free), else MOE_ERR_UNSUPPORTED.  G <= 2048, K <= 131071 (the int32 sum),
  * M and G N below 2^30.  M = 0: nothing is done.
@@ -521,7 +523,8 @@ MOE_API int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, int6
  * q: the rows of the hidden activation, kept in fp32 until then, quantised as
  * moe_quantize_i8 does.  Row strides ldw1 (w1 and w3) and ldw2; biases fp32 or
  * NULL (NULL for SWIGLU); ys device (M, Dout), row stride ldys, `out_dtype`; offsets, limits,
- * alignment, rows outside the groups and the status word as moe_matmul_i8.
+ * alignment, rows outside the groups and the status word as moe_matmul_i8 (where
+ * offsets run backwards, ys of the rows from offsets[G] on is undefined).
  *   workspace >= moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout)
  *   bytes on a 16-byte boundary, one per call in flight.
  */

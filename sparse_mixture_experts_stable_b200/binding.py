@@ -730,8 +730,11 @@ def _elsewhere(dev: torch.device, stream) -> bool:
 
 
 @contextlib.contextmanager
-def _there(dev: torch.device, stream):
-    """Makes the device, and the stream if given, current; yields the caller's stream if it is another one."""
+def _there(dev: torch.device, stream, *tensors):
+    """Makes the device, and the stream if given, current; yields the caller's stream if it is another one.
+
+    ``tensors`` (None among them) are the caller's: the allocator waits for the stream before it reuses their memory.
+    """
     with torch.cuda.device(dev):
         if stream is None:
             yield None
@@ -739,6 +742,9 @@ def _there(dev: torch.device, stream):
             if stream.device != dev:
                 raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
             caller = torch.cuda.current_stream(dev)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
             with torch.cuda.stream(stream):
                 yield caller
 
@@ -835,8 +841,8 @@ def _sort_args(selected, E):
     if selected.dim() not in (1, 2) or not selected.is_contiguous():
         raise ValueError("selected must be a contiguous (T,) or (T, k) tensor")
     T, k = selected.shape if selected.dim() == 2 else (selected.shape[0], 1)
-    if E < 1:
-        raise ValueError("E must be positive")
+    if not 1 <= E < 1 << 31:
+        raise ValueError("E must be positive and fit in 32 bits")
     return dev, T, k
 
 
@@ -857,7 +863,7 @@ def moe_sort(selected: torch.Tensor, E: int, x: Optional[torch.Tensor] = None, o
             raise ValueError("x must be (T, D)")
         dt, D, ldx = _dt(x), x.shape[1], _ld("x", x)
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, selected, x, dev_status, workspace, *(out or {}).values()) as caller:
             o = moe_sort(selected, E, x, out, dev_status, workspace)
             _keep(caller, *(t for name, t in o.items() if out is None or out.get(name) is None))
             return o
@@ -891,7 +897,7 @@ def moe_sort_i8(selected: torch.Tensor, E: int, x: torch.Tensor, out: Optional[d
         raise ValueError("x must be (T, D)")
     dt, D, ldx = _dt(x), x.shape[1], _ld("x", x)
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, selected, x, dev_status, workspace, *(out or {}).values()) as caller:
             o = moe_sort_i8(selected, E, x, out, dev_status, workspace)
             _keep(caller, *(t for name, t in o.items() if out is None or out.get(name) is None))
             return o
@@ -940,7 +946,7 @@ def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor
     if base is not None:
         ldb = _ld("base", _take("base", base, dev, ys.dtype, (T, N)))
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, ys, row, gates, base, y, dev_status) as caller:
             r = moe_unsort(ys, row, gates, base, y, dev_status)
             _keep(caller if y is None else None, r)
             return r
@@ -981,7 +987,7 @@ def moe_unsort_backward(dy: torch.Tensor, ys: Optional[torch.Tensor], row: torch
         rows = T * k if dys is None else dys.shape[0]
     g, gdt = _gates(gates, dev, T, k)
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, dy, ys, row, gates, dys, dgates, dev_status) as caller:
             r = moe_unsort_backward(dy, ys, row, gates, rows, want_dys, want_dgates, dys, dgates, dev_status)
             _keep(caller, None if dys is not None else r[0], None if dgates is not None else r[1])
             return r
@@ -1022,7 +1028,7 @@ def moe_quantize_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Op
     dt = _dt(x)
     M, ldx = (lead[0], _ld("x", x)) if len(lead) == 1 else (math.prod(lead), max(K, 1))
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, x, q, scale, dev_status) as caller:
             r = moe_quantize_i8(x, q, scale, dev_status)
             _keep(caller, None if q is not None else r[0], None if scale is not None else r[1])
             return r
@@ -1127,7 +1133,7 @@ def moe_matmul_i8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wsca
     b = _bias_i8("bias", bias, dev, G, N)
     dtype, dt = _out_dt(out, out_dtype)
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, xq, xscale, wq, wscale, offsets, bias, out, dev_status, workspace) as caller:
             r = moe_matmul_i8(xq, xscale, wq, wscale, offsets, bias, out, out_dtype, dev_status, workspace)
             _keep(caller if out is None else None, r)
             return r
@@ -1189,7 +1195,7 @@ def moe_expert_ffn_i8(kind: str, xq: torch.Tensor, xscale: torch.Tensor, offsets
     pb1, pb2 = _bias_i8("b1", b1, dev, G, n1), _bias_i8("b2", b2, dev, G, Dout)
     dtype, dt = _out_dt(ys, out_dtype)
     if _elsewhere(dev, stream):
-        with _there(dev, stream) as caller:
+        with _there(dev, stream, xq, xscale, offsets, w1, s1, b1, w2, s2, b2, w3, s3, ys, dev_status, workspace) as caller:
             r = moe_expert_ffn_i8(kind, xq, xscale, offsets, w1, s1, b1, w2, s2, b2, w3, s3, ys, out_dtype, dev_status,
                                   workspace)
             _keep(caller if ys is None else None, r)

@@ -197,12 +197,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     pdl_next();
-    // tiles before each group; offsets that run backwards leave the group empty
     for (int g = threadIdx.x; g <= p.G; g += kThreads) s_off[g] = row_offset(p, g);
     __syncthreads();
+    // Offsets that run backwards become their running maximum: no row has two groups, and the tiles fit in an int.
+    bool back = false;
+    for (int g = threadIdx.x; g < p.G; g += kThreads) back |= s_off[g + 1] < s_off[g];
+    if (__syncthreads_or(back)) {
+        if (threadIdx.x == 0) {
+            set_status(p.status, MOE_ERR_BAD_INDEX);
+            for (int g = 0; g < p.G; ++g) s_off[g + 1] = max(s_off[g + 1], s_off[g]);
+        }
+        __syncthreads();
+    }
+    // tiles before each group
     for (int g = threadIdx.x; g < p.G; g += kThreads) {
         const int r = s_off[g + 1] - s_off[g];
-        if (r < 0) set_status(p.status, MOE_ERR_BAD_INDEX);
         const int span = token_span(r, p.max_span);
         s_prefix[g] = r > 0 ? (r + span - 1) / span * p.f_tiles : 0;
     }
@@ -241,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint8_t* st = smem + stage * kStageBytes;
                     tma_load_2d_pair(st, &tmW, kb * kBK, w_y, fb);
                     if (EPI == I8_SWIGLU) tma_load_2d_pair(st + kWBytes / 2, &tmW2, kb * kBK, w_y, fb);
-                    if (nbox == 4)  // most often: one copy is issued faster than four
+                    if (nbox == 4)  // most often, and only if max_span is kNT: one copy is issued faster than four
                         tma_load_2d_pair(st + kWBytes, &tmX128, kb * kBK, x_y, fb);
                     else
                         for (int b = 0; b < nbox; ++b)
@@ -380,7 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(tempty_l + 8u * acc, 0);
             };
-            // v[i][j][e]: row gl + 8 i, token 16 c + 8 j + c2 + e of this warp's 64
+            // v[i][j][e]: row gl + 8 i, token 16 c + 8 j + c2 + e of this warp's 64.  The weight's scale first: tokens
+            // may be very large or small, and the scales' product could leave fp32's range where the result does not.
             const auto sums = [&](int c, float (&v)[4][2][2]) {
                 uint32_t raw[16];
                 tmem_ld_32x16(tmem + 16u * (uint32_t)c, raw);
@@ -392,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float x = __shfl_sync(0xffffffffu, c < 2 ? cur.xs[0] : cur.xs[1], (16 * c + 8 * j + c2 + e) & 31);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[i][j][e] = (float)(int)raw[8 * (i >> 1) + 4 * j + 2 * (i & 1) + e] * (cur.ws[i] * x);
+                            v[i][j][e] = (float)(int)raw[8 * (i >> 1) + 4 * j + 2 * (i & 1) + e] * cur.ws[i] * x;
                     }
             };
             // eight lanes of consecutive features: a whole sector
@@ -617,7 +627,7 @@ extern "C" int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, i
                              int64_t N, int64_t K, void* out, int64_t ldo, moe_dtype out_dtype, int32_t* dev_status,
                              void* workspace, size_t workspace_bytes, moe_stream_t stream) {
     const size_t need = moe_matmul_i8_workspace_size(M, G, N, K);
-    MOE_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), MOE_ERR_WORKSPACE);
+    MOE_REQUIRE(need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need), MOE_ERR_WORKSPACE);
     I8Problem p{};
     p.x = xq, p.xscale = xscale, p.M = M, p.ldx = ldx, p.offsets = offsets, p.w = wq, p.wscale = wscale;
     p.ldw = ldw, p.bias = bias, p.G = G, p.N = N, p.K = K, p.out = out, p.ldo = ldo, p.out_dtype = out_dtype;
@@ -645,7 +655,8 @@ extern "C" int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const floa
     MOE_REQUIRE(ffn_sizes_ok(kind, G, M, D, F, Dout), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(kind != MOE_FFN_SWIGLU || (!b1 && !b2), MOE_ERR_INVALID_ARG);
     if (M == 0) return MOE_OK;
-    MOE_REQUIRE(workspace && workspace_bytes >= moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout),
+    MOE_REQUIRE(workspace && aligned16(workspace) &&
+                    workspace_bytes >= moe_expert_ffn_i8_workspace_size(kind, G, M, D, F, Dout),
                 MOE_ERR_WORKSPACE);
     I8Problem p{};
     p.x = xq, p.xscale = xscale, p.M = M, p.ldx = ldx, p.offsets = offsets, p.w = w1, p.wscale = s1, p.ldw = ldw1;
@@ -663,7 +674,6 @@ extern "C" int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const floa
     float* hscale = reinterpret_cast<float*>(ws);
     int8_t* hq = reinterpret_cast<int8_t*>(ws + align_up((size_t)M * sizeof(float), 256));
     float* h = reinterpret_cast<float*>(hq + align_up((size_t)M * round16(F), 256));
-    MOE_REQUIRE(aligned16(ws), MOE_ERR_INVALID_ARG);
     p.N = F, p.out = h, p.ldo = F, p.out_dtype = MOE_F32;
     if (kind == MOE_FFN_SWIGLU) p.w2 = w3, p.wscale2 = s3, p.epilogue = I8_SWIGLU;
     else p.bias = b1, p.epilogue = I8_GELU;

@@ -124,15 +124,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
     pdl_next();
+    bool back = false;
     for (int g = threadIdx.x; g < p.G; g += kThreads) {
         int lo = 0, hi = (int)p.M;
         if (p.offsets) lo = min(max(p.offsets[g], 0), hi), hi = min(max(p.offsets[g + 1], 0), hi);
-        if (hi < lo) set_status(p.status, MOE_ERR_BAD_INDEX);
+        back |= hi < lo;
         s_off[g] = lo;
         s_end[g] = hi;
         s_prefix[g] = hi > lo ? (hi - lo + sp.tok - 1) / sp.tok : 0;
     }
-    __syncthreads();
+    if (__syncthreads_or(back)) {  // offsets that run backwards become their running maximum: no row has two groups
+        if (threadIdx.x == 0) {
+            set_status(p.status, MOE_ERR_BAD_INDEX);
+            for (int g = 0, run = 0; g < p.G; ++g) {
+                s_off[g] = max(s_off[g], run);
+                run = s_end[g] = max(s_end[g], s_off[g]);
+                s_prefix[g] = (s_end[g] - s_off[g] + sp.tok - 1) / sp.tok;
+            }
+        }
+        __syncthreads();
+    }
     block_scan<kThreads>(s_prefix, p.G);
     const int64_t units = (int64_t)s_prefix[p.G] * sp.fblocks;
     const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (t >= nt) continue;
             const float x = s_scale[t];
-            float u = (float)sa * (wsa * x), v = (float)sc * (wsc * x);
+            float u = (float)sa * wsa * x, v = (float)sc * wsc * x;  // in this order: the scales' product could leave fp32
             TO* out = static_cast<TO*>(p.out) + (int64_t)(t0 + t) * p.ldo;
             if (EPI == I8_SWIGLU) {
                 if (fa < p.N) out[fa] = from_f32<TO>(swiglu_f(u, v));

@@ -364,7 +364,7 @@ size_t sort_workspace(int64_t T, int32_t k, int32_t E) {
 int row_vector(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t D, size_t es) {
     const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | (uintptr_t)(D * es) |
                           (uintptr_t)(lda * es) | (uintptr_t)(ldb * es);
-    return (all & 15) == 0 ? 4 : (all & 3) == 0 ? 2 : (all & 1) == 0 ? 1 : 0;
+    return (all & 15) == 0 ? 4 : (all & 3) == 0 ? 2 : 1;
 }
 
 int launch_scatter(SortParams p, size_t es, cudaStream_t stream) {
@@ -426,7 +426,7 @@ int sort_run(SortParams p, int op, moe_dtype dtype, void* workspace, size_t work
     }
     if (s.small) return sort_small(p, op, dtype, stream);
 
-    MOE_REQUIRE(workspace && workspace_bytes >= sort_workspace(p.T, p.k, p.E), MOE_ERR_WORKSPACE);
+    MOE_REQUIRE(workspace && aligned16(workspace) && workspace_bytes >= sort_workspace(p.T, p.k, p.E), MOE_ERR_WORKSPACE);
     int32_t* hist = static_cast<int32_t*>(workspace);
     p.hist = hist, p.n_super = (int)s.n_super;
     int rc = launch_pdl(hist_kernel, s.n_super, kHistThreads, sizeof(int) * p.E, stream, p, hist);

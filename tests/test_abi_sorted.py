@@ -110,3 +110,11 @@ def test_the_binding_takes_cuda_tensors_only():
             call()
     with pytest.raises(ValueError):
         moe.moe_expert_ffn_i8("relu", q, x[:, 0], None, q, x[:, 0])
+
+
+@pytest.mark.parametrize("call,args", [
+    (sort, dict(T=5000, ws=ODD)), (sort_i8, dict(T=5000, ws=ODD)), (matmul, dict(G=16, off=P, M=4096, wk=ODD)),
+    (ffn, dict(ws=ODD)), (ffn, dict(kind=0, M=4096, ws=ODD)),
+])
+def test_a_workspace_off_its_boundary(call, args):
+    assert call(moe.lib(), **args) == WS
