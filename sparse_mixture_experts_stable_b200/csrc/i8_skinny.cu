@@ -32,7 +32,8 @@ namespace {
 constexpr int kWarps = 8;                      // that multiply; one more loads
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRows = 16;                      // weight rows of a warp
-constexpr int kSeg = 256;                      // bytes of each in a stage
+constexpr int kSeg = 256;                      // bytes of each in a stage,
+constexpr int kHalf = 128;                     // in two swizzled halves
 constexpr int kStageBytes = kWarps * kRows * kSeg;
 constexpr int kStages = 5;
 constexpr int kTok = 16;                 // tokens in shared memory at a time, at most
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_prefix[kMaxG + 1], s_off[kMaxG], s_end[kMaxG];
     __shared__ float s_scale[kTok];
     __shared__ int s_red[2][kWarps][8][32];
-    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 127) & ~uintptr_t(127));
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_x = ring + kRingBytes;
     const I8Problem& p = sp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,9 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int parts = min(sp.ksplit, sp.segs - seg);
                     uint8_t* dst = ring + stage * kStageBytes;
                     tc::mbar_expect_tx(&s_full[stage], (uint32_t)(parts * rows * kSeg));
-                    for (int k = 0; k < parts; ++k, dst += rows * kSeg) {
-                        tc::tma_load_2d(dst, &tm_w, (seg + k) * kSeg, row, &s_full[stage]);
-                        if (EPI == I8_SWIGLU) tc::tma_load_2d(dst + half * kSeg, &tm_w2, (seg + k) * kSeg, row, &s_full[stage]);
+                    for (int k = 0; k < 2 * parts; ++k, dst += rows * kHalf) {
+                        tc::tma_load_2d(dst, &tm_w, seg * kSeg + k * kHalf, row, &s_full[stage]);
+                        if (EPI == I8_SWIGLU) tc::tma_load_2d(dst + half * kHalf, &tm_w2, seg * kSeg + k * kHalf, row, &s_full[stage]);
                     }
                     used |= 1u << stage;
                     last = (last & ~(1u << stage)) | phase << stage;
@@ -189,9 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------- products --------------------------------
     const int kpart = warp % sp.ksplit, team = warp / sp.ksplit;
     // this warp's place in a stage: its piece of the depth, its rows (for SwiGLU those of gate; up's follow all of gate's)
-    const int w_at = kpart * teams * kRows * kSeg + team * FROWS * kSeg, w_second = EPI == I8_SWIGLU ? teams * FROWS * kSeg : 8 * kSeg;
+    const int w_half = teams * kRows * kHalf;  // from the first 128 bytes of the piece's rows to the second
+    const int w_at = kpart * 2 * w_half + team * FROWS * kHalf, w_second = (EPI == I8_SWIGLU ? teams * FROWS : 8) * kHalf;
     bool dead = false;  // a wait timed out (status set): nothing more is written, the barriers are kept
-    const int gl = lane >> 2, q = lane & 3;  // fragment row (weight row, token) and 16-byte column of this lane
+    const int gl = lane >> 2, q = lane & 3;  // fragment row (token) and 16-byte column of this lane
+    // Weight row of the fragment row: those that are read together, an even and the next one, are four apart, so the
+    // swizzle (16-byte column ^ row) puts them in different banks.
+    const int wl = gl >> 1 | (gl & 1) << 2;
     uint32_t phase = 0;
     int stage = 0, item = -1, t0 = 0, nt = 0;
     for (int unit = u0; unit < u1; ++unit) {
@@ -216,6 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) s_scale[t] = r.scale;
                 }
             } else {
+                float scale = 0.f;
+                if (threadIdx.x < nt) scale = p.xscale[t0 + threadIdx.x];
                 // pieces of all tokens, four per thread on their way
                 const int per = (sp.xpitch - 64) / 16;
                 for (int i0 = threadIdx.x; i0 < nt * per; i0 += 4 * kWarps * 32) {
@@ -235,13 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i < nt * per) *reinterpret_cast<uint4*>(s_x + t * sp.xpitch + c) = v[u];
                     }
                 }
-                if (threadIdx.x < nt) s_scale[threadIdx.x] = p.xscale[t0 + threadIdx.x];
+                if (threadIdx.x < nt) s_scale[threadIdx.x] = scale;
             }
             part_sync(kWarps + 1, kWarps * 32);
         }
         const int64_t f0 = ((int64_t)use.fb * teams + team) * FROWS;
-        // features of this lane's sums: weight rows gl and gl + 8
-        const int64_t fa = f0 + gl, fc = EPI == I8_SWIGLU ? fa : fa + 8;
+        // features of this lane's sums: weight rows wl and wl + 8
+        const int64_t fa = f0 + wl, fc = EPI == I8_SWIGLU ? fa : fa + 8;
         float wsa = 0.f, wsc = 0.f, ba = 0.f, bc = 0.f;
         if (fa < p.N) wsa = p.wscale[use.g * p.N + fa];
         if (fc < p.N) wsc = (EPI == I8_SWIGLU ? p.wscale2 : p.wscale)[use.g * p.N + fc];
@@ -253,14 +260,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int seg = kpart; seg - kpart < sp.segs; seg += sp.ksplit) {
             if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(&s_full[stage], phase, p.status));
             if (seg < sp.segs) {
-                const uint8_t* wr = ring + stage * kStageBytes + w_at + gl * kSeg + q * 16;
+                const uint8_t* wr = ring + stage * kStageBytes + w_at + wl * kHalf;
                 const uint8_t* xr = s_x + gl * sp.xpitch + seg * kSeg + q * 16;
                 // beyond K the weights' pieces hold zeros
                 uint4 a[kSeg / 64], c[kSeg / 64], b[kSeg / 64];
 #pragma unroll
                 for (int i = 0; i < kSeg / 64; ++i) {
-                    a[i] = *reinterpret_cast<const uint4*>(wr + 64 * i);
-                    c[i] = *reinterpret_cast<const uint4*>(wr + w_second + 64 * i);
+                    const uint8_t* w = wr + (i >> 1) * w_half + ((q + 4 * (i & 1)) ^ wl) * 16;
+                    a[i] = *reinterpret_cast<const uint4*>(w);
+                    c[i] = *reinterpret_cast<const uint4*>(w + w_second);
                     b[i] = *reinterpret_cast<const uint4*>(xr + 64 * i);
                 }
 #pragma unroll
@@ -331,7 +339,7 @@ int launch(const I8Problem& p, cudaStream_t stream) {
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !attr_set[dev]) {
         MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)(128 + kRingBytes + kTokBytes)));
+                                          (int)(1024 + kRingBytes + kTokBytes)));
         if (dev < 64) attr_set[dev] = true;
     }
     SkinnyParams sp{};
@@ -355,9 +363,9 @@ int launch(const I8Problem& p, cudaStream_t stream) {
     CUtensorMap mw, mw2;
     constexpr bool dual = EPI == I8_SWIGLU;
     const int box = kWarps / sp.ksplit * (dual ? kRows / 2 : kRows);
-    MOE_REQUIRE(make_map_i8(&mw, p.w, p.K, p.G * p.N, p.ldw, box, true), MOE_ERR_CUDA);
-    if (dual) MOE_REQUIRE(make_map_i8(&mw2, p.w2, p.K, p.G * p.N, p.ldw, box, true), MOE_ERR_CUDA);
-    return launch_pdl(kernel, units < sms ? units : sms, kThreads, 128 + kRingBytes + (size_t)sp.tok * sp.xpitch + kSeg, stream,
+    MOE_REQUIRE(make_map_i8(&mw, p.w, p.K, p.G * p.N, p.ldw, box), MOE_ERR_CUDA);
+    if (dual) MOE_REQUIRE(make_map_i8(&mw2, p.w2, p.K, p.G * p.N, p.ldw, box), MOE_ERR_CUDA);
+    return launch_pdl(kernel, units < sms ? units : sms, kThreads, 1024 + kRingBytes + (size_t)sp.tok * sp.xpitch + kSeg, stream,
                       mw, dual ? mw2 : mw, sp);
 }
 
