@@ -23,7 +23,9 @@ __device__ __forceinline__ void block_scan(int* v, int E) {
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll
+    for (int w = 0; w < THREADS / 32 - 1; ++w)  // all at once
+        if (w < warp) before += s_warp[w];
     int run = before + inc - sum;
     for (int i = b; i < b + per && i < E; ++i) {
         const int c = v[i];

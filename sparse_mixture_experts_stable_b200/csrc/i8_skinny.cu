@@ -78,12 +78,15 @@ __device__ __forceinline__ void part_sync(int barrier, int threads) {
 // A place in the sequence of units: item (tokens of a group) and feature block.
 struct Cursor {
     int item, fb, g;
-    // prefix[g]: the items before group g
-    __device__ __forceinline__ void seek(int unit, int fblocks, const int* prefix, int G) {
+    // prefix[g]: the items before group g.  By the 32 lanes of a warp together: the last group whose items do not begin
+    // behind this one, in a 32nd of the groups, then in that.
+    __device__ __forceinline__ void seek(int unit, int fblocks, const int* prefix, int G, int lane) {
         item = unit / fblocks;
         fb = unit - item * fblocks;
-        g = 0;
-        find(prefix, G);
+        const int stride = (G + 31) / 32;  // up to 32, as G is up to kMaxG
+        const int part = __popc(__ballot_sync(0xffffffffu, lane * stride < G && prefix[lane * stride] <= item)) - 1;
+        const int at = part * stride + lane;
+        g = part * stride - 1 + __popc(__ballot_sync(0xffffffffu, lane < stride && at < G && prefix[at] <= item));
     }
     __device__ __forceinline__ void next(int fblocks, const int* prefix, int G) {
         if (++fb < fblocks) return;
@@ -146,12 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
     block_scan<kThreads>(s_prefix, p.G);
-    const int64_t units = (int64_t)s_prefix[p.G] * sp.fblocks;
-    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    // in 32 bits: 64-bit divisions take 800 cycles here
+    const uint32_t units = (uint32_t)s_prefix[p.G] * (uint32_t)sp.fblocks;
+    const uint32_t share = units / gridDim.x, more = units - share * gridDim.x;
+    const int u0 = (int)(share * blockIdx.x + min(blockIdx.x, more)), u1 = u0 + (int)(share + (blockIdx.x < more ? 1 : 0));
     if (u0 >= u1) return;
 
     Cursor use;
-    use.seek(u0, sp.fblocks, s_prefix, p.G);
+    use.seek(u0, sp.fblocks, s_prefix, p.G, lane);
     if (warp == kWarps) {
         // -------------------------------- loads --------------------------------
         if (lane == 0) {
