@@ -501,8 +501,8 @@ MOE_API int moe_quantize_i8(const void* x, moe_dtype dtype, int64_t M, int64_t K
  *   wq        device int8 (G, N, K), row stride ldw (groups N ldw apart); wscale fp32 (G, N).
  *   bias      device fp32 (G, N) or NULL.
  *   out       device (M, N), row stride ldo, `out_dtype`.
- *   workspace device, >= moe_matmul_i8_workspace_size(M, G, N, K) bytes (which may be 0) on a
- *             16-byte boundary, one per call in flight.
+ *   workspace device, >= moe_matmul_i8_workspace_size(M, G, N, K) bytes (which may be 0, and is for
+ *             G = 1) on a 16-byte boundary, one per call in flight.
  * xq and wq start on 16 bytes with row strides of multiples of 16 (K itself is
  * free), else MOE_ERR_UNSUPPORTED.  G <= 2048, K <= 131071 (the int32 sum),
  * M and G N below 2^30.  M = 0: nothing is done.

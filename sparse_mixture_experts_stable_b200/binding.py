@@ -824,6 +824,8 @@ def _out(o: dict, name: str, shape, dtype, dev):
 
 def _padded(rows_shape, K: int, dev) -> torch.Tensor:
     """int8 (*rows_shape, K) whose rows start on multiples of 16 bytes."""
+    if K % 16 == 0:
+        return torch.empty(*rows_shape, K, dtype=torch.int8, device=dev)
     strides = [1, -(-K // 16) * 16]
     for n in reversed(rows_shape[1:]):
         strides.append(strides[-1] * n)
@@ -844,6 +846,17 @@ def _sort_args(selected, E):
     if not 1 <= E < 1 << 31:
         raise ValueError("E must be positive and fit in 32 bits")
     return dev, T, k
+
+
+def _sort_out(out, E, T, k, dev):
+    if out is None:  # the usual case
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        row = torch.empty(T, k, dtype=torch.int32, device=dev)
+        source = torch.empty(T * k, dtype=torch.int32, device=dev)
+        return {"offsets": offsets, "row": row, "source": source}, offsets, row, source
+    o = dict(out)
+    return (o, _out(o, "offsets", (E + 1,), torch.int32, dev), _out(o, "row", (T, k), torch.int32, dev),
+            _out(o, "source", (T * k,), torch.int32, dev))
 
 
 def moe_sort(selected: torch.Tensor, E: int, x: Optional[torch.Tensor] = None, out: Optional[dict] = None,
@@ -867,10 +880,7 @@ def moe_sort(selected: torch.Tensor, E: int, x: Optional[torch.Tensor] = None, o
             o = moe_sort(selected, E, x, out, dev_status, workspace)
             _keep(caller, *(t for name, t in o.items() if out is None or out.get(name) is None))
             return o
-    o = {} if out is None else dict(out)
-    offsets = _out(o, "offsets", (E + 1,), torch.int32, dev)
-    row = _out(o, "row", (T, k), torch.int32, dev)
-    source = _out(o, "source", (T * k,), torch.int32, dev)
+    o, offsets, row, source = _sort_out(out, E, T, k, dev)
     xs = None
     if x is not None:
         xs = o.get("xs")
@@ -901,10 +911,7 @@ def moe_sort_i8(selected: torch.Tensor, E: int, x: torch.Tensor, out: Optional[d
             o = moe_sort_i8(selected, E, x, out, dev_status, workspace)
             _keep(caller, *(t for name, t in o.items() if out is None or out.get(name) is None))
             return o
-    o = {} if out is None else dict(out)
-    offsets = _out(o, "offsets", (E + 1,), torch.int32, dev)
-    row = _out(o, "row", (T, k), torch.int32, dev)
-    source = _out(o, "source", (T * k,), torch.int32, dev)
+    o, offsets, row, source = _sort_out(out, E, T, k, dev)
     xscale = _out(o, "xscale", (T * k,), torch.float32, dev)
     xq = o.get("xq")
     if xq is None:
@@ -1033,15 +1040,15 @@ def moe_quantize_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Op
             _keep(caller, None if q is not None else r[0], None if scale is not None else r[1])
             return r
     if q is None:
-        q = _padded(lead, K, dev)
+        q, ldq = _padded(lead, K, dev), -(-K // 16) * 16
     else:
-        _take("q", q, dev, torch.int8, x.shape)
+        ldq = _ld3("q", _take("q", q, dev, torch.int8, x.shape), 1)
     if scale is None:
         scale = torch.empty(*lead, dtype=torch.float32, device=dev)
     else:
         _take("scale", scale, dev, torch.float32, tuple(lead), contiguous=True)
-    _check("moe_quantize_i8", lib().moe_quantize_i8(x.data_ptr(), dt, M, K, ldx, q.data_ptr(), _ld3("q", q, 1),
-                                                    scale.data_ptr(), _status(dev_status, dev), _raw_stream(dev.index)))
+    _check("moe_quantize_i8", lib().moe_quantize_i8(x.data_ptr(), dt, M, K, ldx, q.data_ptr(), ldq, scale.data_ptr(),
+                                                    _status(dev_status, dev), _raw_stream(dev.index)))
     return q, scale
 
 
@@ -1081,7 +1088,7 @@ def _weight_i8(name, w, scale, dev, G, N, K):
     _take("the weight's scale", scale, dev, torch.float32, None, True)
     if scale.numel() != G * N:
         raise ValueError(f"{name} needs {G * N} scales, got {scale.numel()}")
-    return _ld3(name, w, 16)
+    return K if K % 16 == 0 and w.is_contiguous() else _ld3(name, w, 16)
 
 
 def _rows_i8(xq, xscale, offsets):
@@ -1142,7 +1149,8 @@ def moe_matmul_i8(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Tensor, wsca
         ldo = max(N, 1)
     else:
         ldo = _ld("out", _take("out", out, dev, dtype, (M, N)))
-    ws = _scratch(lib().moe_matmul_i8_workspace_size(M, G, N, K), dev, workspace)
+    # one group needs no workspace
+    ws = _scratch(lib().moe_matmul_i8_workspace_size(M, G, N, K) if G > 1 else 0, dev, workspace)
     _check("moe_matmul_i8", lib().moe_matmul_i8(xq.data_ptr(), xscale.data_ptr(), M, _ld("xq", xq, 16), _ptr(offsets),
                                                 wq.data_ptr(), wscale.data_ptr(), ldw, b, G, N, K, out.data_ptr(), ldo, dt,
                                                 _status(dev_status, dev), _ptr(ws), _nbytes(ws), _raw_stream(dev.index)))
