@@ -9,13 +9,19 @@
 // rows.  One thread fills a ring of kStages stages of 32 KB, 256 bytes of each row, by TMA:
 // up to 160 KB are in flight per SM whatever the arithmetic takes.  (Rings of the warps' own
 // took 8 to 16 copies for the same 32 KB; the SM issues one in some 70 cycles, and that was
-// as long as the memory needs.)  256 bytes per row want no swizzle, so the reads of the
-// fragments meet two-way bank conflicts.  Products are m16n8k32 of the warp-level tensor
-// instructions on 8-bit integers: a tenth of the weights' time, so tcgen05 has nothing to
-// win here.  The order of k is free as long as both operands share it, so a lane's four
-// bytes of each fragment are neighbours and come in 16-byte reads.  With fp32 rows (the
-// experts' hidden rows) every block quantises the rows that it stages: a few KB, against a
-// launch and a round trip through memory.
+// as long as the memory needs.)  A row's 256 bytes lie in two swizzled halves, and the rows
+// that a warp reads together are chosen so that they meet no bank conflict: with unswizzled
+// rows of 256 bytes a stage took 900 cycles of shared memory, and the memory brings one in
+// 1400 (103 experts of 2048 x 512 26.4 us, now 24.2; of 1024 x 2048 40.1, now 38.4).
+// Products are m16n8k32 of the warp-level tensor instructions on 8-bit integers: a tenth of
+// the weights' time, so tcgen05 has nothing to win here.  The order of k is free as long as
+// both operands share it, so a lane's four bytes of each fragment are neighbours and come in
+// 16-byte reads.  With fp32 rows (the experts' hidden rows) every block quantises the rows
+// that it stages: a few KB, against a launch and a round trip through memory.
+// What bounds it: the weights stream at 6.7 TB/s (one row times 131072 x 2048: 46 us); a
+// launch costs 7 us besides: 1.7 us until the first copy is asked for (offsets, their scan),
+// 2 until it is there and the tokens are staged, the last unit and the launch itself.  Two
+// sets of eight warps that take the stages in turn gained nothing (26.2 us and 40.9).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,7 +50,6 @@ constexpr size_t kTokBytes = (size_t)kTok * (2048 + 64) + kSeg;  // the last pie
 
 struct SkinnyParams {
     I8Problem p;
-    int K16;      // 16-byte pieces of a row
     int segs;     // kSeg-byte pieces of a row
     int xpitch;   // bytes between tokens in shared memory, 64 modulo 128
     int tok;      // tokens in shared memory at a time: 8 or 16
@@ -349,7 +354,6 @@ int launch(const I8Problem& p, cudaStream_t stream) {
     }
     SkinnyParams sp{};
     sp.p = p;
-    sp.K16 = (int)((p.K + 15) / 16);
     sp.segs = (int)((p.K + kSeg - 1) / kSeg);
     sp.xpitch = (int)((p.K + 127) / 128 * 128 + 64);
     sp.tok = p.K <= 2048 ? kTok : kTok / 2;
