@@ -326,6 +326,46 @@ __global__ void __launch_bounds__(kI8Threads) scatter_i8_kernel(const SortParams
         if (rows[j] >= 0) p.xscale[rows[j]] = scale;
 }
 
+// The same for rows of up to STEPS steps of a warp: one holds its token's row in registers.
+template <typename T, int STEPS>
+__global__ void __launch_bounds__(kI8Threads) scatter_i8_warp_kernel(const SortParams p) {
+    constexpr int kStride = 32 * kChunk<T>;
+    const int lane = threadIdx.x & 31, first = lane * kChunk<T>;
+    const int64_t t = (int64_t)blockIdx.x * (kI8Threads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_next();
+    if (t >= p.T) return;
+    int rows[kMaxK / 32];
+#pragma unroll
+    for (int h = 0; h < kMaxK / 32; ++h) rows[h] = lane + 32 * h < p.k ? p.row[t * p.k + lane + 32 * h] : -1;
+    const T* src = static_cast<const T*>(p.x) + t * p.ldx;
+    Raw<T> x[STEPS];
+    uint32_t m = 0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+        if (s * kStride < p.D) x[s].load(src + first + s * kStride, p.D - first - s * kStride, p.vecx);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+        if (s * kStride < p.D) m = x[s].max_bits(m);
+    const RowQuant r = row_quant(__reduce_max_sync(0xffffffffu, Raw<T>::join(m)), p.status, lane == 0);
+    uint32_t o[STEPS][kChunk<T> / 4];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+        if (s * kStride < p.D) quantize_chunk(x[s], r, o[s]);
+#pragma unroll
+    for (int h = 0; h < kMaxK / 32; ++h) {
+        for (int j = 0; j < 32 && j + 32 * h < p.k; ++j) {
+            const int row = __shfl_sync(0xffffffffu, rows[h], j);
+            if (row < 0) continue;
+            int8_t* q = static_cast<int8_t*>(p.xs) + (int64_t)row * p.ldxs + first;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                if (first + s * kStride < p.D) store_chunk(q + s * kStride, o[s], p.D - first - s * kStride, p.vecq);
+        }
+        if (rows[h] >= 0) p.xscale[rows[h]] = r.scale;
+    }
+}
+
 // super-blocks, or the one-launch form's blocks, for T tokens of k assignments
 struct SortPlan {
     bool small;
@@ -382,8 +422,10 @@ int launch_scatter(SortParams p, size_t es, cudaStream_t stream) {
 template <typename T>
 int launch_scatter_i8(const SortParams& p, cudaStream_t stream) {
     constexpr int kPer = kI8Threads / 32;
-    if (p.D <= 32 * kChunk<T> * 2 || !aligned16(p.xs) || p.ldxs % 16)
-        return launch_pdl(scatter_i8_kernel<T, false>, (p.T + kPer - 1) / kPer, kI8Threads, 0, stream, p);
+    const int64_t warps = (p.T + kPer - 1) / kPer;
+    if (p.D <= 32 * kChunk<T> * 4) return launch_pdl(scatter_i8_warp_kernel<T, 4>, warps, kI8Threads, 0, stream, p);
+    if (p.D <= 32 * kChunk<T> * 8) return launch_pdl(scatter_i8_warp_kernel<T, 8>, warps, kI8Threads, 0, stream, p);
+    if (!aligned16(p.xs) || p.ldxs % 16) return launch_pdl(scatter_i8_kernel<T, false>, warps, kI8Threads, 0, stream, p);
     const size_t smem = align_up((size_t)(p.D < kI8Seg ? p.D : kI8Seg), 16);
     return launch_pdl(scatter_i8_kernel<T, true>, p.T, kI8Threads, smem, stream, p);
 }
