@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kResident = 3;  // blocks of teams per SM
 
 struct QuantParams {
     const void* x;
@@ -48,20 +49,22 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_block_kernel(const Quant
     if (threadIdx.x == 0) p.scale[r] = s;
 }
 
-// One warp per row of up to STEPS steps, held in registers while the warp's next row is on its way: a row's loads
-// otherwise wait for the arithmetic and the stores of the row before.  131072 x 512 fp32: 54 us, 5.0 TB/s of rows read
-// (86 with a row per warp and block); 16384 x 2048 bf16: 21 us, 4.8 TB/s.
-template <int STEPS, typename T>
-__global__ void __launch_bounds__(kThreads, STEPS > 4 ? 2 : 3) quantize_warp_kernel(const QuantParams p) {
-    constexpr int kStride = 32 * kChunk<T>;
-    const int lane = threadIdx.x & 31, first = lane * kChunk<T>;
-    const int64_t step = (int64_t)gridDim.x * kWarps;
+// TEAM warps per row of up to four steps of the team, held in registers while the team's next row is on its way: a row's
+// loads otherwise wait for the arithmetic and the stores of the row before.  131072 x 512 fp32: 54 us, 5.0 TB/s of rows read
+// (86 with a row per warp and block); 16384 x 2048 bf16 20 us, 5.1 TB/s with what is written, fp32 29.5 us, 5.7 TB/s (44
+// with a block per row); 16384 x 8192 bf16 67 us (78).  Eight steps of half as many warps: fp32 4096 60 us instead of 56.
+template <int TEAM, typename T>
+__global__ void __launch_bounds__(kThreads, kResident) quantize_team_kernel(const QuantParams p) {
+    constexpr int STEPS = 4, kStride = 32 * TEAM * kChunk<T>;
+    __shared__ uint32_t s_max[2][kWarps];  // rows take them in turn
+    const int warp = threadIdx.x >> 5, team = warp / TEAM, tid = threadIdx.x % (32 * TEAM), first = tid * kChunk<T>;
+    const int64_t step = (int64_t)gridDim.x * (kWarps / TEAM);
     pdl_wait();
     pdl_next();
     int64_t lo, hi;
     row_range(p, lo, hi);
     const T* x = static_cast<const T*>(p.x);
-    int64_t r = lo + (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    int64_t r = lo + (int64_t)blockIdx.x * (kWarps / TEAM) + team;
     Raw<T> next[STEPS];
     const auto load = [&](int64_t row) {
 #pragma unroll
@@ -69,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, STEPS > 4 ? 2 : 3) quantize_warp_ker
             if (s * kStride < p.K) next[s].load(x + row * p.ldx + first + s * kStride, p.K - first - s * kStride, p.vecx);
     };
     if (r < hi) load(r);
-    for (; r < hi; r += step) {
+    for (int turn = 0; r < hi; r += step, turn ^= 1) {
         Raw<T> row[STEPS];
         uint32_t m = 0;
 #pragma unroll
@@ -78,7 +81,14 @@ __global__ void __launch_bounds__(kThreads, STEPS > 4 ? 2 : 3) quantize_warp_ker
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
             if (s * kStride < p.K) m = row[s].max_bits(m);
-        const RowQuant rq = row_quant(__reduce_max_sync(0xffffffffu, Raw<T>::join(m)), p.status, lane == 0);
+        m = __reduce_max_sync(0xffffffffu, Raw<T>::join(m));
+        if constexpr (TEAM > 1) {
+            if ((threadIdx.x & 31) == 0) s_max[turn][warp] = m;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");
+#pragma unroll
+            for (int w = 0; w < TEAM; ++w) m = max(m, s_max[turn][team * TEAM + w]);
+        }
+        const RowQuant rq = row_quant(m, p.status, tid == 0);
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int c = first + s * kStride;
@@ -88,20 +98,25 @@ __global__ void __launch_bounds__(kThreads, STEPS > 4 ? 2 : 3) quantize_warp_ker
                 store_chunk(p.q + r * p.ldq + c, o, p.K - c, p.vecq);
             }
         }
-        if (lane == 0) p.scale[r] = rq.scale;
+        if (tid == 0) p.scale[r] = rq.scale;
     }
+}
+
+template <int TEAM, typename T>
+int launch_team(const QuantParams& p, cudaStream_t stream) {
+    const int64_t most = device_sm_count() * kResident, need = (p.M + kWarps / TEAM - 1) / (kWarps / TEAM);
+    return launch_pdl(quantize_team_kernel<TEAM, T>, need < most ? need : most, kThreads, 0, stream, p);
 }
 
 template <typename T>
 int launch(const QuantParams& p, cudaStream_t stream) {
-    const int64_t sms = device_sm_count();
-    const int64_t warp_rows = (p.M + kWarps - 1) / kWarps;
-    const auto grid = [&](int resident) { return warp_rows < sms * resident ? warp_rows : sms * resident; };
-    constexpr int kShort = 4, kLong = sizeof(T) == 2 ? 8 : 12;
-    if (p.K <= 32 * kChunk<T> * kShort) return launch_pdl(quantize_warp_kernel<kShort, T>, grid(3), kThreads, 0, stream, p);
-    // a warp each where the rows fill the card's warps and a warp's registers hold one; else a block each
-    if (p.K <= 32 * kChunk<T> * kLong && p.M >= sms * 2 * kWarps)
-        return launch_pdl(quantize_warp_kernel<kLong, T>, grid(2), kThreads, 0, stream, p);
+    constexpr int kStep = 32 * kChunk<T>;  // values of a warp's step
+    if (p.K <= kStep * 4) return launch_team<1, T>(p, stream);
+    // longer rows by the teams whose registers hold one, where they are enough for all of them; else a block each
+    const int64_t warps = device_sm_count() * 2 * kWarps;
+    if (p.K <= kStep * 8 && p.M >= warps / 2) return launch_team<2, T>(p, stream);
+    if (p.K <= kStep * 16 && p.M >= warps / 4) return launch_team<4, T>(p, stream);
+    if (p.K <= kStep * 32 && p.M >= warps / 8) return launch_team<8, T>(p, stream);
     return launch_pdl(quantize_block_kernel<T>, p.M, kThreads, 0, stream, p);
 }
 

@@ -178,7 +178,7 @@ __device__ __forceinline__ void store_chunk(int8_t* p, const uint32_t (&w)[W], i
 template <int WARPS, typename T>
 __device__ __forceinline__ uint32_t row_max(const T* src, int64_t D, bool vecx, uint32_t* s_max) {
     constexpr int kStride = 32 * WARPS * kChunk<T>;
-    constexpr int kBatch = WARPS == 1 ? 8 : 2;
+    constexpr int kBatch = WARPS == 8 ? 4 : 8;
     const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x;
     uint32_t m = 0;
     for (int64_t c = tid * kChunk<T>; c < D; c += kBatch * kStride) {

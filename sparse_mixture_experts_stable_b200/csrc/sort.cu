@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(const SortParams p, i
 constexpr int kI8Threads = 128;
 constexpr int kI8Seg = 8192;  // values of a row in shared memory at a time
 
-// The same in 8 bits: a block per token quantises its row into shared memory, from where each warp writes every fourth
-// of the token's rows.  Where the rows do not lie on 16 bytes, or are no longer than a warp's eight steps, a warp per
-// token writes them as it goes.
+// The same in 8 bits, for rows too long for scatter_i8_team_kernel: a block per token quantises its row into shared memory,
+// from where each warp writes every fourth of the token's rows.  Where the rows do not lie on 16 bytes a warp per token
+// writes them as it goes.
 template <typename T, bool SHARED>
 __global__ void __launch_bounds__(kI8Threads) scatter_i8_kernel(const SortParams p) {
     __shared__ uint32_t s_max[kI8Threads / 32];
@@ -326,12 +326,16 @@ __global__ void __launch_bounds__(kI8Threads) scatter_i8_kernel(const SortParams
         if (rows[j] >= 0) p.xscale[rows[j]] = scale;
 }
 
-// The same for rows of up to STEPS steps of a warp: one holds its token's row in registers.
-template <typename T, int STEPS>
-__global__ void __launch_bounds__(kI8Threads) scatter_i8_warp_kernel(const SortParams p) {
-    constexpr int kStride = 32 * kChunk<T>;
-    const int lane = threadIdx.x & 31, first = lane * kChunk<T>;
-    const int64_t t = (int64_t)blockIdx.x * (kI8Threads / 32) + (threadIdx.x >> 5);
+// The same for rows of up to four steps of a team of TEAM warps, which holds its token's row in registers and quantises it
+// once.  T = 16384, rows alone: bf16 D = 2048 24 us with k = 1 and 56 with k = 8 (32 and 61 through shared memory), D = 1024
+// 10.5 and 30 (23 and 38); fp32 D = 2048 32 and 65 (45 and 72).  Eight steps of four warps instead of shared memory gain at
+// fp32 D = 4096 (130 -> 127 us, k = 8) and lose at bf16 D = 8192 (85 -> 98, k = 1).
+template <typename T, int TEAM>
+__global__ void __launch_bounds__(kI8Threads) scatter_i8_team_kernel(const SortParams p) {
+    constexpr int STEPS = 4, kStride = 32 * TEAM * kChunk<T>;
+    __shared__ uint32_t s_max[kI8Threads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x % (32 * TEAM), first = tid * kChunk<T>;
+    const int64_t t = (int64_t)blockIdx.x * (kI8Threads / 32 / TEAM) + warp / TEAM;
     pdl_wait();
     pdl_next();
     if (t >= p.T) return;
@@ -347,7 +351,16 @@ __global__ void __launch_bounds__(kI8Threads) scatter_i8_warp_kernel(const SortP
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
         if (s * kStride < p.D) m = x[s].max_bits(m);
-    const RowQuant r = row_quant(__reduce_max_sync(0xffffffffu, Raw<T>::join(m)), p.status, lane == 0);
+    m = __reduce_max_sync(0xffffffffu, Raw<T>::join(m));
+    if constexpr (TEAM > 1) {
+        if (lane == 0) s_max[warp] = m;
+        // constant barriers: with one in a register a block is given all 16, and fewer blocks are resident
+        if (TEAM == 4 || warp < TEAM) asm volatile("bar.sync 1, %0;" ::"n"(32 * TEAM) : "memory");
+        else asm volatile("bar.sync 2, %0;" ::"n"(32 * TEAM) : "memory");
+#pragma unroll
+        for (int w = 0; w < TEAM; ++w) m = max(m, s_max[warp / TEAM * TEAM + w]);
+    }
+    const RowQuant r = row_quant(m, p.status, tid == 0);
     uint32_t o[STEPS][kChunk<T> / 4];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(kI8Threads) scatter_i8_warp_kernel(const SortP
             for (int s = 0; s < STEPS; ++s)
                 if (first + s * kStride < p.D) store_chunk(q + s * kStride, o[s], p.D - first - s * kStride, p.vecq);
         }
-        if (rows[h] >= 0) p.xscale[rows[h]] = r.scale;
+        if (tid < 32 && rows[h] >= 0) p.xscale[rows[h]] = r.scale;
     }
 }
 
@@ -423,8 +436,10 @@ template <typename T>
 int launch_scatter_i8(const SortParams& p, cudaStream_t stream) {
     constexpr int kPer = kI8Threads / 32;
     const int64_t warps = (p.T + kPer - 1) / kPer;
-    if (p.D <= 32 * kChunk<T> * 4) return launch_pdl(scatter_i8_warp_kernel<T, 4>, warps, kI8Threads, 0, stream, p);
-    if (p.D <= 32 * kChunk<T> * 8) return launch_pdl(scatter_i8_warp_kernel<T, 8>, warps, kI8Threads, 0, stream, p);
+    constexpr int kStep = 32 * kChunk<T>;
+    if (p.D <= kStep * 4) return launch_pdl(scatter_i8_team_kernel<T, 1>, warps, kI8Threads, 0, stream, p);
+    if (p.D <= kStep * 8) return launch_pdl(scatter_i8_team_kernel<T, 2>, (p.T + 1) / 2, kI8Threads, 0, stream, p);
+    if (p.D <= kStep * 16) return launch_pdl(scatter_i8_team_kernel<T, 4>, p.T, kI8Threads, 0, stream, p);
     if (!aligned16(p.xs) || p.ldxs % 16) return launch_pdl(scatter_i8_kernel<T, false>, warps, kI8Threads, 0, stream, p);
     const size_t smem = align_up((size_t)(p.D < kI8Seg ? p.D : kI8Seg), 16);
     return launch_pdl(scatter_i8_kernel<T, true>, p.T, kI8Threads, smem, stream, p);
