@@ -7,7 +7,7 @@ import torch
 import sparse_mixture_experts_stable_b200 as moe
 from sparse_mixture_experts_stable_b200 import binding as B
 from tests.gpu_util import DEV, cpu, cpu64
-from tests.sorted_util import within
+from tests.sorted_util import ref_quantize, ref_sort, routing, within
 from tests.test_gpu_i8 import _dev, _i8, _product, _scale
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +85,28 @@ def test_expert_count_beyond_32_bits():
     for E in (0, -1, (1 << 32) + 1):
         with pytest.raises(ValueError):
             moe.moe_sort(sel, E)
+
+
+# where the kernels change over: rows of 4, 8, 16 and 32 steps of a warp (256 values of bf16, 128 of fp32), odd widths and
+# unaligned rows, up to 64 experts per token, fewer and more rows than the teams
+@pytest.mark.parametrize("dtype,step", [(torch.float32, 128), (torch.bfloat16, 256)])
+@pytest.mark.parametrize("steps,more", [(4, 0), (4, 1), (8, 0), (8, 4), (16, 0), (16, 8), (32, 0), (32, 3)])
+@pytest.mark.parametrize("T,k", [(4200, 1), (1400, 3), (70, 64), (2400, 2)])
+def test_rows_in_8_bits_at_every_width(dtype, step, steps, more, T, k):
+    D, E = step * steps + more, 24
+    rng = np.random.default_rng(D + T)
+    sel = routing(rng, T, k, E, dropped=0.05)
+    x = torch.randn(T, D, generator=torch.Generator().manual_seed(D)).to(dtype)
+    x[5], x[6, 0] = 0, 100.0
+    q, s = ref_quantize(cpu64(x))
+    off, row, _ = ref_sort(sel, E)
+    status = moe.new_status(DEV)
+    got, gs = moe.moe_quantize_i8(x.to(DEV), dev_status=status)
+    np.testing.assert_array_equal(cpu(got), q)
+    np.testing.assert_array_equal(cpu(gs), s.astype(np.float32))
+    r = moe.moe_sort_i8(torch.from_numpy(sel).to(DEV), E, x.to(DEV), dev_status=status)
+    rows, scales = cpu(r["xq"]), cpu(r["xscale"])
+    t, j = np.nonzero(row >= 0)
+    np.testing.assert_array_equal(rows[row[t, j]], q[t])
+    np.testing.assert_array_equal(scales[row[t, j]], s.astype(np.float32)[t])
+    assert off[-1] == len(t) and moe.moe_read_status(status) == 0
