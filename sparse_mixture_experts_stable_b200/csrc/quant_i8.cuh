@@ -18,10 +18,10 @@
 // exact where it matters.
 // A row of zeros has scale 0.  A row with an infinity or a NaN has scale NaN and q = 0.
 //
-// A team of one or several warps takes a row, 16 bytes per lane and step, twice: for the
+// Rows of up to four 16-byte steps of a team of warps are held in registers
+// (quantize_team_kernel, scatter_i8_team_kernel).  Else a team takes a row twice: for the
 // maximum with kBatch steps in flight, then for q, when the row still lies in the
-// first-level cache.  (Rows of many short-lived warps; quantize_warp_kernel, whose warps go
-// on to another row, holds it in registers and has the next one's loads on their way.)
+// first-level cache.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -83,6 +83,9 @@ struct Raw {
         if (vec && n >= N) {
             const uint4 r = *reinterpret_cast<const uint4*>(p);
             w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+        } else if (sizeof(T) == 2 && n >= N && (reinterpret_cast<uintptr_t>(p) & 3) == 0) {  // 16384 x 2050: 49 -> 36 us
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) set(i, i < n ? p[i] : from_f32<T>(0.f));
@@ -178,7 +181,7 @@ __device__ __forceinline__ void store_chunk(int8_t* p, const uint32_t (&w)[W], i
 template <int WARPS, typename T>
 __device__ __forceinline__ uint32_t row_max(const T* src, int64_t D, bool vecx, uint32_t* s_max) {
     constexpr int kStride = 32 * WARPS * kChunk<T>;
-    constexpr int kBatch = WARPS == 8 ? 4 : 8;
+    constexpr int kBatch = WARPS == 8 ? 4 : 8;  // eight warps' blocks of 64 registers: 16384 x 8192 fp32 119 us, 130 with 8
     const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x;
     uint32_t m = 0;
     for (int64_t c = tid * kChunk<T>; c < D; c += kBatch * kStride) {
