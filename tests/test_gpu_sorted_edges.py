@@ -6,6 +6,7 @@ import torch
 
 import sparse_mixture_experts_stable_b200 as moe
 from sparse_mixture_experts_stable_b200 import binding as B
+from sparse_mixture_experts_stable_b200.layer import SwiGLUMoEInt8
 from tests.gpu_util import DEV, cpu, cpu64
 from tests.sorted_util import ref_quantize, ref_sort, routing, within
 from tests.test_gpu_i8 import _dev, _i8, _product, _scale
@@ -110,3 +111,25 @@ def test_rows_in_8_bits_at_every_width(dtype, step, steps, more, T, k):
     np.testing.assert_array_equal(rows[row[t, j]], q[t])
     np.testing.assert_array_equal(scales[row[t, j]], s.astype(np.float32)[t])
     assert off[-1] == len(t) and moe.moe_read_status(status) == 0
+
+
+def test_layer_captured_with_its_second_stream():
+    T, H, E, F, k, Fs = 40, 256, 16, 128, 4, 96
+    g = torch.Generator().manual_seed(3)
+    mk = lambda *s: (torch.randn(*s, generator=g) * 0.1).to(torch.bfloat16).to(DEV)  # noqa: E731
+    xs = [torch.randn(T, H, generator=g).to(torch.bfloat16).to(DEV) for _ in range(3)]
+    wr, bias = mk(E, H), torch.randn(E, generator=g).to(DEV)
+    experts = SwiGLUMoEInt8.quantize(mk(E, F, H), mk(E, F, H), mk(E, H, F))
+    shared = SwiGLUMoEInt8.quantize(mk(1, Fs, H), mk(1, Fs, H), mk(1, H, Fs))
+    layer = SwiGLUMoEInt8(T, H, E, F, k, F_shared=Fs)
+    want = [layer.forward(x, wr, bias, experts, shared)["y"].clone() for x in xs]
+    x = xs[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer.forward(x, wr, bias, experts, shared)["y"]
+    for i in (1, 2, 0):
+        x.copy_(xs[i])
+        graph.replay()
+        assert torch.equal(y, want[i])
+    assert moe.moe_read_status(layer.status) == 0
