@@ -1082,13 +1082,17 @@ def _ld3(name: str, t: torch.Tensor, unit: int) -> int:
 
 def _weight_i8(name, w, scale, dev, G, N, K):
     """Checks an 8-bit weight (G, N, K) or, for G = 1, (N, K) with its scales; returns the row stride."""
+    if (w is not None and scale is not None and w.shape == (G, N, K) and K % 16 == 0 and w.is_contiguous()
+            and w.dtype is torch.int8 and w.device == dev and scale.device == dev and scale.dtype is torch.float32
+            and scale.numel() == G * N and scale.is_contiguous()):
+        return K  # the usual case
     _take(name, w, dev, torch.int8)
     if w.shape != (G, N, K) and (G != 1 or w.shape != (N, K)):
         raise ValueError(f"{name} must be ({G}, {N}, {K}), got {tuple(w.shape)}")
     _take("the weight's scale", scale, dev, torch.float32, None, True)
     if scale.numel() != G * N:
         raise ValueError(f"{name} needs {G * N} scales, got {scale.numel()}")
-    return K if K % 16 == 0 and w.is_contiguous() else _ld3(name, w, 16)
+    return _ld3(name, w, 16)
 
 
 def _rows_i8(xq, xscale, offsets):
