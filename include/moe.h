@@ -460,6 +460,17 @@ MOE_API int moe_unsort(const void* ys, int64_t ldys, int64_t rows, const int32_t
                        void* y, int64_t ldy, moe_dtype dtype, int32_t* dev_status, moe_stream_t stream);
 
 /*
+ * moe_unsort_ex -- moe_unsort with types of their own for the result and the
+ * base: ys of `dtype`, y of `y_dtype` (the same, or bf16 of fp32 rows), base of
+ * either (any other combination: MOE_ERR_UNSUPPORTED).  Rows that stay in fp32
+ * until here leave the one rounding of the sum.
+ */
+MOE_API int moe_unsort_ex(const void* ys, int64_t ldys, int64_t rows, moe_dtype dtype, const int32_t* row,
+                          const void* gates, moe_dtype gate_dtype, int64_t T, int32_t k, int64_t N, const void* base,
+                          int64_t ldbase, moe_dtype base_dtype, void* y, int64_t ldy, moe_dtype y_dtype,
+                          int32_t* dev_status, moe_stream_t stream);
+
+/*
  * moe_unsort_backward -- the gradients of moe_unsort for a given dy:
  *   dys[row[t,j], :] = gate[t,j] * dy[t,:]     (rounded once; rows without a token are not written)
  *   dgates[t,j]      = dy[t,:] . ys[row[t,j], :]   fp32 (T, k), 0 where row[t,j] < 0

@@ -44,7 +44,7 @@ EXPORTED = [
     "moe_backward_gelu_workspace_size", "moe_backward_gelu", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine",
     "moe_ipc_export", "moe_ipc_import", "moe_ipc_close", "moe_expert_ffn_save", "moe_wait_probe",
     "moe_swiglu_layer_workspace_size", "moe_swiglu_layer_forward", "moe_sort_workspace_size", "moe_sort", "moe_sort_i8",
-    "moe_unsort", "moe_unsort_backward", "moe_quantize_i8", "moe_matmul_i8_workspace_size", "moe_matmul_i8",
+    "moe_unsort", "moe_unsort_ex", "moe_unsort_backward", "moe_quantize_i8", "moe_matmul_i8_workspace_size", "moe_matmul_i8",
     "moe_expert_ffn_i8_workspace_size", "moe_expert_ffn_i8",
 ]
 IPC_HANDLE_BYTES = 64
@@ -153,6 +153,8 @@ def lib():
                                   _vp, _vp, _vp, _sz, _vp]
         L.moe_unsort.argtypes = [_vp, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _i32, _i64, _vp, _i64, _vp, _i64,
                                  ctypes.c_int, _vp, _vp]
+        L.moe_unsort_ex.argtypes = [_vp, _i64, _i64, ctypes.c_int, _vp, _vp, ctypes.c_int, _i64, _i32, _i64, _vp, _i64,
+                                    ctypes.c_int, _vp, _i64, ctypes.c_int, _vp, _vp]
         L.moe_unsort_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _i32, _i64, _vp,
                                           _i64, _vp, ctypes.c_int, _vp, _vp]
         L.moe_quantize_i8.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]
@@ -935,10 +937,13 @@ def _gates(gates, dev, T, k):
 
 def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor] = None,
                base: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
-               dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+               dev_status: Optional[torch.Tensor] = None, stream=None,
+               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """y[t] = base[t] + sum_j gates[t, j] * ys[row[t, j]] over row >= 0 (fixed j order, fp32 accumulation).
 
     ``ys`` (rows, N); ``row`` int32 (T, k) from ``moe_sort``; without gates the sum is the gradient of ``moe_sort``.
+    y has ys's type, or bf16 (``out_dtype``, or the given y's) where ys is fp32: the sum is then the only rounding, by
+    ``moe_unsort_ex``.  base has the type of ys or of y.
     """
     dev = _dev(ys)
     if ys.dim() != 2:
@@ -949,21 +954,35 @@ def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor
         raise ValueError("row must be (T, k)")
     T, k = row.shape
     g, gdt = _gates(gates, dev, T, k)
-    ldb = 0
+    dtype = ys.dtype
+    if y is not None or out_dtype is not None:
+        if y is not None:
+            _take("y", y, dev, shape=(T, N))
+        dtype = _out_dt(y, out_dtype)[0]
+        if dtype is not ys.dtype and dt != MOE_F32:
+            raise TypeError(f"y must be {ys.dtype}, got {dtype}")
+    ldb, bdt = 0, dt
     if base is not None:
-        ldb = _ld("base", _take("base", base, dev, ys.dtype, (T, N)))
+        ldb, bdt = _ld("base", _take("base", base, dev, shape=(T, N))), _dt(base)
+        if base.dtype is not ys.dtype and base.dtype is not dtype:
+            raise TypeError(f"base must be {dtype}, got {base.dtype}")
     if _elsewhere(dev, stream):
         with _there(dev, stream, ys, row, gates, base, y, dev_status) as caller:
-            r = moe_unsort(ys, row, gates, base, y, dev_status)
+            r = moe_unsort(ys, row, gates, base, y, dev_status, out_dtype=dtype)
             _keep(caller if y is None else None, r)
             return r
     if y is None:
-        y = torch.empty(T, N, dtype=ys.dtype, device=dev)
+        y = torch.empty(T, N, dtype=dtype, device=dev)
         ldy = max(N, 1)
     else:
-        ldy = _ld("y", _take("y", y, dev, ys.dtype, (T, N)))
-    _check("moe_unsort", lib().moe_unsort(ys.data_ptr(), _ld("ys", ys), R, row.data_ptr(), g, gdt, T, k, N, _ptr(base), ldb,
-                                          y.data_ptr(), ldy, dt, _status(dev_status, dev), _raw_stream(dev.index)))
+        ldy = _ld("y", y)
+    if dtype is ys.dtype:
+        _check("moe_unsort", lib().moe_unsort(ys.data_ptr(), _ld("ys", ys), R, row.data_ptr(), g, gdt, T, k, N, _ptr(base), ldb,
+                                              y.data_ptr(), ldy, dt, _status(dev_status, dev), _raw_stream(dev.index)))
+    else:
+        _check("moe_unsort_ex", lib().moe_unsort_ex(ys.data_ptr(), _ld("ys", ys), R, dt, row.data_ptr(), g, gdt, T, k, N,
+                                                    _ptr(base), ldb, bdt, y.data_ptr(), ldy, _dt(y),
+                                                    _status(dev_status, dev), _raw_stream(dev.index)))
     return y
 
 

@@ -16,6 +16,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "block_scan.cuh"
 #include "common.cuh"
 #include "quant_i8.cuh"
@@ -497,7 +499,7 @@ int sort_run(SortParams p, int op, moe_dtype dtype, void* workspace, size_t work
 
 // ------------------------------- and back -----------------------------------
 
-// V: 16 or 4 bytes, or one value, of a row of T; its values as fp32
+// V: 16 or 4 bytes, or one value, of a row of T (8 bytes of bf16 beside 16 of fp32); its values as fp32
 template <typename T, typename V>
 struct Vec {
     static constexpr int kN = sizeof(V) / sizeof(T);
@@ -514,6 +516,11 @@ struct Vec {
         return r;
     }
 };
+
+// BYTES consecutive bytes
+template <int BYTES>
+using Bytes = std::conditional_t<BYTES == 16, uint4,
+                                 std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, uint16_t>>>;
 
 struct UnsortParams {
     const void* ys;
@@ -588,10 +595,13 @@ __device__ __forceinline__ void add_rows(const T* ys, int64_t ldys, const int* s
 
 // y[t] = base[t] + sum_j gate ys[row], j ascending, in fp32.  `split` warps share a token's columns; a warp takes U
 // vectors per lane at a time and J rows, so that J x U loads are in flight: without that the rows come one latency
-// after another.
-template <typename T, typename G, typename V, int J, int U>
+// after another.  Types: T of ys, TB of base, TY of y.  fp32 rows into bf16 tokens round each sum once; rows in bf16 halve
+// the bytes and round every term first.  T = 16384, k = 8, D = 2048: 174 us and 104; T = 16: 2.4 both.
+template <typename T, typename G, typename V, int J, int U, typename TB, typename TY>
 __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) {
     constexpr int N = Vec<T, V>::kN;
+    using VB = Bytes<N * sizeof(TB)>;
+    using VY = Bytes<N * sizeof(TY)>;
     __shared__ int s_row[kWarps][kMaxK];
     __shared__ float s_gate[kWarps][kMaxK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -602,8 +612,8 @@ __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) 
     if (t >= p.T) return;
     const int n = token_rows<G>(p, t, lane, s_row[warp], s_gate[warp]);
     const T* ys = static_cast<const T*>(p.ys);
-    const T* base = p.base ? static_cast<const T*>(p.base) + t * p.ldbase : nullptr;
-    T* y = static_cast<T*>(p.y) + t * p.ldy;
+    const TB* base = p.base ? static_cast<const TB*>(p.base) + t * p.ldbase : nullptr;
+    TY* y = static_cast<TY*>(p.y) + t * p.ldy;
     for (int64_t c0 = (unit - t * p.split) * (32 * N * U); c0 < p.N; c0 += (int64_t)p.split * (32 * N * U)) {
         int64_t col[U];
         float acc[U][N];
@@ -615,11 +625,11 @@ __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) 
             for (int e = 0; e < N; ++e) acc[u][e] = 0.f;
         }
         if (base) {
-            V r[U];
+            VB r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = *reinterpret_cast<const V*>(base + col[u]);
+            for (int u = 0; u < U; ++u) r[u] = *reinterpret_cast<const VB*>(base + col[u]);
 #pragma unroll
-            for (int u = 0; u < U; ++u) Vec<T, V>::unpack(r[u], acc[u]);
+            for (int u = 0; u < U; ++u) Vec<TB, VB>::unpack(r[u], acc[u]);
         }
         int j = 0;
         for (; n - j >= J; j += J) add_rows<T, V, J, U>(ys, p.ldys, s_row[warp], s_gate[warp], j, col, acc);
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(kThreads) unsort_kernel(const UnsortParams p) 
         if (n - j >= 1) add_rows<T, V, 1, U>(ys, p.ldys, s_row[warp], s_gate[warp], j, col, acc);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + 32 * N * u + lane * N < p.N) *reinterpret_cast<V*>(y + col[u]) = Vec<T, V>::pack(acc[u]);
+            if (c0 + 32 * N * u + lane * N < p.N) *reinterpret_cast<VY*>(y + col[u]) = Vec<TY, VY>::pack(acc[u]);
     }
 }
 
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const UnsortP
 
 constexpr int kFill = 16;  // warps per SM that a short batch is spread over
 
-template <typename T, typename G, typename V, int J, int U>
+template <typename T, typename G, typename V, int J, int U, typename TB, typename TY>
 int launch_unsort(UnsortParams p, cudaStream_t stream) {
     const int64_t groups = (p.N + 32 * Vec<T, V>::kN * U - 1) / (32 * Vec<T, V>::kN * U);
     // two warps per token at least, of wide rows: T = 16384, k = 8, D = 2048 bf16 118 us with one, 115 with two, 120 with
@@ -700,7 +710,7 @@ int launch_unsort(UnsortParams p, cudaStream_t stream) {
     const int64_t want = fill < least ? least : fill;
     p.split = (int)(want < groups ? want : groups);
     const int64_t grid = (p.T * p.split + kWarps - 1) / kWarps;
-    return launch_pdl(unsort_kernel<T, G, V, J, U>, grid, kThreads, 0, stream, p);
+    return launch_pdl(unsort_kernel<T, G, V, J, U, TB, TY>, grid, kThreads, 0, stream, p);
 }
 
 template <typename T, typename G, typename V, int U, int TEAM>
@@ -717,36 +727,47 @@ int launch_backward(const UnsortParams& p, cudaStream_t stream) {
 // to an odd row's start took 228 and 449.)  Loads at a time: 8 vectors, for narrower ones 16 on the way back; the gradient
 // 4 of each operand, for fp32 values 8 (D = 1001: 221 us, 263 with 4; bf16 D = 2046: 284 us with 8).
 // The gradient of rows of up to eight vectors: eight lanes each (D = 64: 9 us, 44 with a warp each).
-template <typename T, typename G, typename V, int X>
+template <typename T, typename G, typename V, int X, typename TB, typename TY>
 int launch_back(const UnsortParams& p, bool backward, cudaStream_t stream) {
-    if (backward)
-        return p.N <= 8 * Vec<T, V>::kN ? launch_backward<T, G, V, 1, 8>(p, stream) : launch_backward<T, G, V, sizeof(T) == 2 ? 4 : 4 * X, 32>(p, stream);
-    if (p.k >= 6) return launch_unsort<T, G, V, 8, X>(p, stream);
-    if (p.k >= 3) return launch_unsort<T, G, V, 4, 2 * X>(p, stream);
-    return launch_unsort<T, G, V, 2, 4 * X>(p, stream);
+    if constexpr (std::is_same_v<T, TB> && std::is_same_v<T, TY>)  // the gradient's tensors have one type
+        if (backward)
+            return p.N <= 8 * Vec<T, V>::kN ? launch_backward<T, G, V, 1, 8>(p, stream)
+                                            : launch_backward<T, G, V, sizeof(T) == 2 ? 4 : 4 * X, 32>(p, stream);
+    if (p.k >= 6) return launch_unsort<T, G, V, 8, X, TB, TY>(p, stream);
+    if (p.k >= 3) return launch_unsort<T, G, V, 4, 2 * X, TB, TY>(p, stream);
+    return launch_unsort<T, G, V, 2, 4 * X, TB, TY>(p, stream);
 }
 
-template <typename T, typename G>
+template <typename T, typename G, typename TB = T, typename TY = T>
 int launch_back(const UnsortParams& p, bool backward, int bytes, cudaStream_t stream) {
-    if (bytes == 16) return launch_back<T, G, uint4, 1>(p, backward, stream);
+    if (bytes == 16) return launch_back<T, G, uint4, 1, TB, TY>(p, backward, stream);
     if constexpr (sizeof(T) == 2)
-        if (bytes < 4) return launch_back<T, G, uint16_t, 2>(p, backward, stream);
-    return launch_back<T, G, uint32_t, 2>(p, backward, stream);
+        if (bytes < 4) return launch_back<T, G, uint16_t, 2, TB, TY>(p, backward, stream);
+    return launch_back<T, G, uint32_t, 2, TB, TY>(p, backward, stream);
 }
 
-int unsort_run(const UnsortParams& p, bool backward, moe_dtype dtype, moe_dtype gate_dtype, cudaStream_t stream) {
+// dtype: of ys and the gradient's tensors
+int unsort_run(const UnsortParams& p, bool backward, moe_dtype dtype, moe_dtype gate_dtype, moe_dtype base_dtype,
+               moe_dtype y_dtype, cudaStream_t stream) {
     const size_t es = dtype_size(dtype);
-    const uintptr_t all = reinterpret_cast<uintptr_t>(p.ys) | reinterpret_cast<uintptr_t>(p.base) |
-                          reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.dy) |
-                          (uintptr_t)(p.N * es) | (uintptr_t)(p.ldys * es) | (uintptr_t)(p.ldy * es) |
-                          (uintptr_t)(p.ldbase * es) | (uintptr_t)(p.lddy * es);
+    // a vector of ys is as many values of the others: their addresses and strides in bytes of ys' type
+    const auto at = [&](const void* a, int64_t ld, moe_dtype t) {
+        return (uintptr_t)(reinterpret_cast<uintptr_t>(a) * (es / dtype_size(t))) | (uintptr_t)(ld * es);
+    };
+    const uintptr_t all = at(p.ys, p.ldys, dtype) | at(p.base, p.ldbase, base_dtype) | at(p.y, p.ldy, y_dtype) |
+                          at(p.dy, p.lddy, dtype) | (uintptr_t)(p.N * es);
     const int bytes = (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 2;
     const bool gb = gate_dtype == MOE_BF16;
+    using bf16 = __nv_bfloat16;
     if (dtype == MOE_BF16)
-        return gb ? launch_back<__nv_bfloat16, __nv_bfloat16>(p, backward, bytes, stream)
-                  : launch_back<__nv_bfloat16, float>(p, backward, bytes, stream);
-    return gb ? launch_back<float, __nv_bfloat16>(p, backward, bytes, stream)
-              : launch_back<float, float>(p, backward, bytes, stream);
+        return gb ? launch_back<bf16, bf16>(p, backward, bytes, stream) : launch_back<bf16, float>(p, backward, bytes, stream);
+    if (y_dtype == MOE_F32)
+        return gb ? launch_back<float, bf16>(p, backward, bytes, stream) : launch_back<float, float>(p, backward, bytes, stream);
+    if (base_dtype == MOE_F32)
+        return gb ? launch_back<float, bf16, float, bf16>(p, false, bytes, stream)
+                  : launch_back<float, float, float, bf16>(p, false, bytes, stream);
+    return gb ? launch_back<float, bf16, bf16, bf16>(p, false, bytes, stream)
+              : launch_back<float, float, bf16, bf16>(p, false, bytes, stream);
 }
 
 }  // namespace
@@ -793,19 +814,31 @@ extern "C" int moe_sort_i8(const int64_t* selected, int64_t T, int32_t k, int32_
     return sort_run(p, ROW_I8, dtype, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" int moe_unsort(const void* ys, int64_t ldys, int64_t rows, const int32_t* row, const void* gates,
-                          moe_dtype gate_dtype, int64_t T, int32_t k, int64_t N, const void* base, int64_t ldbase,
-                          void* y, int64_t ldy, moe_dtype dtype, int32_t* dev_status, moe_stream_t stream) {
-    MOE_REQUIRE(valid_dtype(dtype) && valid_dtype(gate_dtype), MOE_ERR_INVALID_ARG);
+extern "C" int moe_unsort_ex(const void* ys, int64_t ldys, int64_t rows, moe_dtype dtype, const int32_t* row,
+                             const void* gates, moe_dtype gate_dtype, int64_t T, int32_t k, int64_t N, const void* base,
+                             int64_t ldbase, moe_dtype base_dtype, void* y, int64_t ldy, moe_dtype y_dtype,
+                             int32_t* dev_status, moe_stream_t stream) {
+    MOE_REQUIRE(valid_dtype(dtype) && valid_dtype(gate_dtype) && valid_dtype(base_dtype) && valid_dtype(y_dtype),
+                MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(T >= 0 && k >= 1 && N >= 1 && rows >= 0 && ldys >= N && ldy >= N, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(T == 0 || (row && y), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE((rows == 0 || ys) && (!base || ldbase >= N), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(k <= kMaxK && T < (int64_t(1) << 30) && T * k < (int64_t(1) << 30), MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(y_dtype == dtype || dtype == MOE_F32, MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(!base || base_dtype == dtype || base_dtype == y_dtype, MOE_ERR_UNSUPPORTED);
     if (T == 0) return MOE_OK;
     UnsortParams p{};
     p.ys = ys, p.ldys = ldys, p.rows = rows, p.row = row, p.gates = gates, p.T = T, p.k = k, p.N = N;
     p.base = base, p.ldbase = base ? ldbase : 0, p.y = y, p.ldy = ldy, p.status = dev_status;
-    return unsort_run(p, false, dtype, gate_dtype, reinterpret_cast<cudaStream_t>(stream));
+    return unsort_run(p, false, dtype, gate_dtype, base ? base_dtype : dtype, y_dtype,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_unsort(const void* ys, int64_t ldys, int64_t rows, const int32_t* row, const void* gates,
+                          moe_dtype gate_dtype, int64_t T, int32_t k, int64_t N, const void* base, int64_t ldbase,
+                          void* y, int64_t ldy, moe_dtype dtype, int32_t* dev_status, moe_stream_t stream) {
+    return moe_unsort_ex(ys, ldys, rows, dtype, row, gates, gate_dtype, T, k, N, base, ldbase, dtype, y, ldy, dtype,
+                         dev_status, stream);
 }
 
 extern "C" int moe_unsort_backward(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t rows,
@@ -823,5 +856,5 @@ extern "C" int moe_unsort_backward(const void* dy, int64_t lddy, const void* ys,
     p.ys = dgates ? ys : nullptr, p.ldys = dgates ? ldys : 0, p.rows = rows, p.row = row, p.gates = gates;
     p.T = T, p.k = k, p.N = N, p.y = dys, p.ldy = dys ? lddys : 0, p.dy = dy, p.lddy = lddy, p.dgates = dgates;
     p.status = dev_status;
-    return unsort_run(p, true, dtype, gate_dtype, reinterpret_cast<cudaStream_t>(stream));
+    return unsort_run(p, true, dtype, gate_dtype, dtype, dtype, reinterpret_cast<cudaStream_t>(stream));
 }

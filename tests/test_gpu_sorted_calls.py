@@ -1,0 +1,104 @@
+"""The sorted rows and the 8-bit products: types, padding, full experts and rows that are not finite, at every kernel that a
+call can reach."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_stable_b200 as moe
+from sparse_mixture_experts_stable_b200.layer import SwiGLUMoEInt8
+from tests.gpu_util import DEV, cpu, cpu64
+from tests.sorted_util import HALF, U, ref_quantize, ref_sort, ref_unsort, routing, within
+from tests.test_gpu_i8 import _ffn_ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# k: each number of rows taken together; N: 16-byte vectors, one value, both ends of a warp's steps
+@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (40, 2, 7), (33, 2, 2048), (600, 4, 132), (300, 17, 264), (700, 8, 1024), (20, 64, 1001)])
+@pytest.mark.parametrize("gates", [None, F32, BF16])
+@pytest.mark.parametrize("base", [None, F32, BF16])
+def test_unsort_of_fp32_rows_into_bf16(T, k, N, gates, base):
+    """The sum is rounded once, whatever the base's type."""
+    rng = np.random.default_rng(T + N)
+    _, row, src = ref_sort(routing(rng, T, k, 24, dropped=0.2), 24)
+    R = max(int((src >= 0).sum()), 1)
+    ys = torch.randn(R, N, generator=torch.Generator().manual_seed(N))
+    g = None if gates is None else torch.from_numpy(rng.uniform(0, 1, (T, k)).astype(np.float32)).to(gates)
+    b = None if base is None else torch.randn(T, N, generator=torch.Generator().manual_seed(T)).to(base)
+    want, mag = ref_unsort(cpu64(ys), row, None if g is None else cpu64(g), None if b is None else cpu64(b), N)
+    sums = k * U * mag * 1.001  # k fused multiply-adds in fp32, each off by U of a partial sum that is at most mag
+    bound = sums + HALF[BF16] * (np.abs(want) + sums)
+    args = ys.to(DEV), torch.from_numpy(row.astype(np.int32)).to(DEV), None if g is None else g.to(DEV)
+    b = None if b is None else b.to(DEV)
+    y = moe.moe_unsort(*args, base=b, out_dtype=BF16)
+    assert y.dtype is BF16
+    within(cpu64(y), want, bound, "y")
+    # rows of wider matrices, on 4 and on 2 bytes
+    wide = torch.full((T, N + 5), 9.0, dtype=BF16, device=DEV)
+    odd = torch.full((R, N + 3), 7.0, device=DEV)
+    odd[:, 1:N + 1] = args[0]
+    moe.moe_unsort(odd[:, 1:N + 1], *args[1:], base=b, y=wide[:, 1:N + 1])
+    assert torch.equal(wide[:, 1:N + 1], y) and (wide[:, 0] == 9).all() and (wide[:, N + 1:] == 9).all()
+
+
+def test_unsort_of_fp32_rows_into_bf16_on_a_stream_and_in_a_graph():
+    row = torch.arange(80, dtype=torch.int32, device=DEV).view(20, 4)
+    ys, base = torch.randn(80, 136, device=DEV), torch.randn(20, 136, device=DEV).to(BF16)
+    want = moe.moe_unsort(ys, row, base=base, out_dtype=BF16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = moe.moe_unsort(ys, row, base=base, out_dtype=BF16, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    src = torch.zeros_like(ys)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = moe.moe_unsort(src, row, base=base, out_dtype=BF16)
+    src.copy_(ys)
+    graph.replay()
+    assert torch.equal(y, want)
+
+
+def test_types_that_unsort_refuses():
+    row = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    f, h = torch.zeros(4, 16, device=DEV), torch.zeros(4, 16, dtype=BF16, device=DEV)
+    for call in (lambda: moe.moe_unsort(h, row, out_dtype=F32), lambda: moe.moe_unsort(h, row, y=f),
+                 lambda: moe.moe_unsort(h, row, base=f), lambda: moe.moe_unsort(f, row, base=h),
+                 lambda: moe.moe_unsort(f, row, y=h, out_dtype=F32), lambda: moe.moe_unsort(f, row, out_dtype=torch.float16),
+                 lambda: moe.moe_unsort(f, row, y=f.half()), lambda: moe.moe_unsort(f, row, base=[0]),
+                 lambda: moe.moe_unsort(f, row, y=h[:3])):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    with pytest.raises(ValueError):
+        SwiGLUMoEInt8(4, 16, 4, 16, 1, dtype=F32, rows_dtype=BF16)
+
+
+@pytest.mark.parametrize("T,H,E,F,k,Fs", [(1, 64, 8, 32, 2, 0), (33, 136, 16, 40, 4, 56), (700, 256, 32, 128, 8, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_layer_rounds_once(T, H, E, F, k, Fs, dtype):
+    """The experts' and the shared expert's rows reach the sum unrounded."""
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).to(dtype).to(DEV)
+    wr, bias = torch.randn(E, H, generator=g).to(dtype).to(DEV), torch.randn(E, generator=g).to(DEV)
+    mk = lambda *s: (torch.randn(*s, generator=g) * 0.1).to(dtype).to(DEV)  # noqa: E731
+    experts = SwiGLUMoEInt8.quantize(mk(E, F, H), mk(E, F, H), mk(E, H, F))
+    shared = SwiGLUMoEInt8.quantize(mk(1, Fs, H), mk(1, Fs, H), mk(1, H, Fs)) if Fs else None
+    layer = SwiGLUMoEInt8(T, H, E, F, k, F_shared=Fs, dtype=dtype)
+    for _ in range(2):  # the buffers are used again
+        o = layer.forward(x, wr, bias, experts, shared)
+    assert moe.moe_read_status(layer.status) == 0 and o["y"].dtype is dtype
+    off, row, src = ref_sort(cpu(o["selected"]), E)
+    q, sc = ref_quantize(cpu64(x))
+    q, sc = torch.from_numpy(q).to(torch.int8), torch.from_numpy(sc).float()
+    to = lambda d: {n: t.cpu() for n, t in d.items()}  # noqa: E731
+    ys, bound = _ffn_ref("swiglu", q[src // k], sc[src // k], off, to(experts), F32)
+    gates = cpu64(o["gates_f32"])[..., None]
+    want, mag, err = (gates * ys[row]).sum(1), (gates * (np.abs(ys) + bound)[row]).sum(1), (gates * bound[row]).sum(1)
+    if Fs:
+        b, eb = _ffn_ref("swiglu", q, sc, [0, T], to(shared), F32)
+        want, mag, err = want + b, mag + np.abs(b) + eb, err + eb
+    err = err + (k + 1) * U * mag
+    within(cpu64(o["y"]), want, err + HALF[dtype] * (np.abs(want) + err), "y")
