@@ -205,8 +205,8 @@ def _run_own(s):
         return moe.moe_matmul_i8(q, scale, s["wq"], s["wscale"], out_dtype=s["dtype"])
     r = moe.moe_sort_i8(s["selected"], c["E"], s["x"])
     ys = moe.moe_expert_ffn_i8("swiglu", r["xq"], r["xscale"], r["offsets"], s["gate"], s["gate_scale"], w2=s["down"],
-                               s2=s["down_scale"], w3=s["up"], s3=s["up_scale"], out_dtype=s["dtype"])
-    return moe.moe_unsort(ys, r["row"], s["gates"])
+                               s2=s["down_scale"], w3=s["up"], s3=s["up_scale"], out_dtype=torch.float32)
+    return moe.moe_unsort(ys, r["row"], s["gates"], out_dtype=s["dtype"])
 
 
 def run(state):
