@@ -434,6 +434,7 @@ MOE_API int moe_sort(const int64_t* selected, int64_t T, int32_t k, int32_t E, c
  * moe_quantize_i8 does it: xq[r,:] = q(x[source[r] / k]) (int8, row stride
  * ldxq >= D; give it a multiple of 16 for moe_matmul_i8) and xscale[r] fp32
  * (T k).  Each token is quantised once.  Columns past D of xq are not written.
+ * A token of which no choice takes part may hold anything: it sets no status.
  * Other arguments, the order and the workspace as moe_sort.
  */
 MOE_API int moe_sort_i8(const int64_t* selected, int64_t T, int32_t k, int32_t E, const void* x, moe_dtype dtype,

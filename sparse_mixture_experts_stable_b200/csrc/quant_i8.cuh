@@ -204,6 +204,14 @@ __device__ __forceinline__ uint32_t row_max(const T* src, int64_t D, bool vecx, 
     return m;
 }
 
+// Whether a row that is not finite has a place to go to; one that has none (a padding token) may hold anything.
+__device__ __forceinline__ bool reports(uint32_t m_bits, const int* rows, int n) {
+    bool any = false;
+    if (m_bits >= 0x7f800000u)
+        for (int j = 0; j < n; ++j) any |= rows[j] >= 0;
+    return any;
+}
+
 // The team quantises the row src[0..D) into rows[0..n) of q (-1: none; row stride ldq) and returns its scale.
 // vecq: q rows start on 8 bytes.  Elements past D of q are not written.
 template <int WARPS, typename T>
@@ -211,7 +219,8 @@ __device__ __forceinline__ float quantize_row(const T* src, int64_t D, const int
                                               bool vecx, bool vecq, uint32_t* s_max, int32_t* status) {
     constexpr int kStride = 32 * WARPS * kChunk<T>;
     const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x;
-    const RowQuant r = row_quant(row_max<WARPS>(src, D, vecx, s_max), status, tid == 0);
+    const uint32_t m = row_max<WARPS>(src, D, vecx, s_max);
+    const RowQuant r = row_quant(m, status, tid == 0 && reports(m, rows, n));
 #pragma unroll 2
     for (int64_t c = tid * kChunk<T>; c < D; c += kStride) {
         Raw<T> x;

@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kI8Threads) scatter_i8_kernel(const SortParams
     int8_t* q = static_cast<int8_t*>(p.xs);
     float scale;
     if constexpr (SHARED) {
-        const RowQuant r = row_quant(row_max<kI8Threads / 32>(src, p.D, p.vecx, s_max), p.status, threadIdx.x == 0);
+        const uint32_t m = row_max<kI8Threads / 32>(src, p.D, p.vecx, s_max);  // its barriers also bring `rows` to all threads
+        const RowQuant r = row_quant(m, p.status, threadIdx.x == 0 && reports(m, rows, p.k));
         scale = r.scale;
         for (int64_t s0 = 0; s0 < p.D; s0 += kI8Seg) {
             const int len = (int)(p.D - s0 < kI8Seg ? p.D - s0 : kI8Seg);
@@ -362,7 +363,14 @@ __global__ void __launch_bounds__(kI8Threads) scatter_i8_team_kernel(const SortP
 #pragma unroll
         for (int w = 0; w < TEAM; ++w) m = max(m, s_max[warp / TEAM * TEAM + w]);
     }
-    const RowQuant r = row_quant(m, p.status, tid == 0);
+    bool report = tid == 0;
+    if (m >= 0x7f800000u) {  // a token without rows may hold anything; it is loaded before they are known, and written nowhere
+        bool any = false;
+#pragma unroll
+        for (int h = 0; h < kMaxK / 32; ++h) any |= rows[h] >= 0;
+        report &= __any_sync(0xffffffffu, any);
+    }
+    const RowQuant r = row_quant(m, p.status, report);
     uint32_t o[STEPS][kChunk<T> / 4];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import sparse_mixture_experts_stable_b200 as moe
+from sparse_mixture_experts_stable_b200 import binding as B
 from sparse_mixture_experts_stable_b200.layer import SwiGLUMoEInt8
 from tests.gpu_util import DEV, cpu, cpu64
 from tests.sorted_util import HALF, U, ref_quantize, ref_sort, ref_unsort, routing, within
@@ -102,3 +103,41 @@ def test_layer_rounds_once(T, H, E, F, k, Fs, dtype):
         want, mag, err = want + b, mag + np.abs(b) + eb, err + eb
     err = err + (k + 1) * U * mag
     within(cpu64(o["y"]), want, err + HALF[dtype] * (np.abs(want) + err), "y")
+
+
+# (T, k, D in steps of a warp, columns before xq): one launch with few and many tokens per block, teams of 1, 2 and 4 warps,
+# rows in shared memory (one segment, two), a warp per token for rows off their boundary
+ROW_KERNELS = [(40, 3, 2.5, 0), (3000, 1, 2.5, 0), (3000, 3, 2.5, 0), (3000, 3, 7, 0), (3000, 3, 13, 0), (1500, 3, 30.5, 0),
+               (1400, 3, 70.5, 0), (3000, 3, 18.25, 3)]
+
+
+def _sort_i8_at(sel, E, x, skip, status):
+    """moe_sort_i8 into rows that begin `skip` bytes after a boundary."""
+    T, D = x.shape
+    if not skip:
+        return moe.moe_sort_i8(sel, E, x, dev_status=status)
+    xq = torch.full((sel.numel(), D + 2 * skip), 77, dtype=torch.int8, device=DEV)[:, skip:skip + D]
+    return moe.moe_sort_i8(sel, E, x, out=dict(xq=xq), dev_status=status)
+
+
+@pytest.mark.parametrize("T,k,steps,skip", ROW_KERNELS)
+@pytest.mark.parametrize("dtype,step", [(F32, 128), (BF16, 256)])
+def test_padding_tokens_may_hold_anything(T, k, steps, skip, dtype, step):
+    """Tokens of which no choice takes part: no status, and the others' rows as without them."""
+    D, E = int(steps * step), 24
+    sel = routing(np.random.default_rng(T + D), T, k, E)
+    pads = [0, 7, T // 2, T - 1]
+    sel[pads] = -1
+    x = torch.randn(T, D, generator=torch.Generator().manual_seed(D)).to(dtype)
+    q, s = ref_quantize(cpu64(x))
+    x[pads[0]], x[pads[1], D - 1], x[pads[2], D // 2], x[pads[3], 0] = float("nan"), float("inf"), float("nan"), -float("inf")
+    _, row, _ = ref_sort(sel, E)
+    status = moe.new_status(DEV)
+    r = _sort_i8_at(torch.from_numpy(sel).to(DEV), E, x.to(DEV), skip, status)
+    t, j = np.nonzero(row >= 0)
+    np.testing.assert_array_equal(cpu(r["xq"])[row[t, j]], q[t])
+    np.testing.assert_array_equal(cpu(r["xscale"])[row[t, j]], s.astype(np.float32)[t])
+    assert moe.moe_read_status(status) == 0
+    sel[pads[2], k - 1] = 5  # one choice is enough
+    _sort_i8_at(torch.from_numpy(sel).to(DEV), E, x.to(DEV), skip, status)
+    assert moe.moe_read_status(status) == B.MOE_ERR_NONFINITE
