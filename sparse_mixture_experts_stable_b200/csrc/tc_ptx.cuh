@@ -147,11 +147,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
 }
 
 // The same without release semantics, for a thread that has nothing to publish: a release waits for all of the
-// thread's global stores first, thousands of cycles after an epilogue's.  `after` is a value that the thread has read
-// before it arrives.
+// thread's global stores first, thousands of cycles after an epilogue's.  `after` is made of the values that the thread has
+// read and that may be overwritten once it has arrived, and is never 0x7fffffff: the arrival is predicated on that, so it is
+// not issued before the reads have returned.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster, uint32_t after) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];  // after %1" ::"r"(bar_cluster), "r"(after)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0x7fffffff;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(bar_cluster),
+        "r"(after)
+        : "memory");
 }
 
 // TMA tile load into this CTA's shared memory whose completion is counted on an

@@ -141,3 +141,26 @@ def test_padding_tokens_may_hold_anything(T, k, steps, skip, dtype, step):
     sel[pads[2], k - 1] = 5  # one choice is enough
     _sort_i8_at(torch.from_numpy(sel).to(DEV), E, x.to(DEV), skip, status)
     assert moe.moe_read_status(status) == B.MOE_ERR_NONFINITE
+
+
+@pytest.mark.parametrize("K", [16, 300])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_thousands_of_short_tiles(K, dtype):
+    """One and three steps of the depth per tile: the tiles' queue is filled and emptied as fast as it can be, and no tile is
+    taken twice or for another."""
+    G, N = 700, 520
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    counts = torch.randint(0, 60, (G,), device=DEV, generator=gen)
+    off = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    M = int(off[-1])
+    assert M > 8 * G  # tiles, not the few-row kernel
+    pad = -(-K // 16) * 16
+    xq = torch.randint(-128, 128, (M, pad), device=DEV, generator=gen).to(torch.int8)[:, :K]
+    wq = torch.randint(-128, 128, (G, N, pad), device=DEV, generator=gen).to(torch.int8)[..., :K]
+    one = torch.ones(G * max(M, N), device=DEV)
+    want = torch.cat([xq[off[g]:off[g + 1]].double() @ wq[g].double().T for g in range(G)])
+    assert want.abs().max() < 2 ** 24  # exact in fp32
+    want = want.to(dtype)
+    for _ in range(20):
+        out = moe.moe_matmul_i8(xq, one[:M], wq, one[:G * N].view(G, N), offsets=off.int(), out_dtype=dtype)
+        assert torch.equal(out, want)
