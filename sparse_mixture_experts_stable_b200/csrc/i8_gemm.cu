@@ -30,7 +30,8 @@
 // as 256 tokens allow.  16384 x 2048 x 2048 bf16: 60 us, 2300 TOPS (torch._int_mm without
 // scales 57); SwiGLU of 131072 rows in 256 groups, 2048 x 512: 300 us; the product back,
 // 512 x 2048: 209 us, half of it the rows' bytes.
-// Every wait is bounded (kWaitLimitNs); after a timeout nothing more is written.
+// Every wait on an mbarrier is bounded (kWaitLimitNs); after a timeout nothing more is written, and the barriers that warps
+// share are still met by all of them.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -235,7 +236,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            for (uint32_t it = 0;; ++it) {
+            bool ok = true;
+            for (uint32_t it = 0; ok; ++it) {
                 const Tile t = take_tile(qfull, s_tile, qempty_l, it, p.status, &s_abort);
                 if (t.g < 0) break;
                 const int half = token_half(t.n);
@@ -246,6 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, p.status)) {
                         s_abort = 1;
+                        ok = false;
                         break;
                     }
                     if (leader) mbar_expect_tx(&full[stage], tx_pair);
@@ -262,6 +265,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
+                }
+            }
+            // The CTA does not end before its copies have landed and the MMAs that read them are done; after a timeout not
+            // before one more wait, much longer than either takes.
+            for (int s = 0; s < kStages && mbar_wait(&empty[stage], phase ^ 1u, p.status); ++s) {
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
@@ -373,8 +384,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return w;
         };
+        // Whether this warp has a tile.  SwiGLU: and its partner, so that neither waits for one that has given up.
+        const int bar = 1 + 2 * r + (q & 1);
+        const auto going = [&](bool mine) {
+            if (EPI != I8_SWIGLU) return mine;
+            uint32_t both;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %2, 0;\n\t"
+                "bar.red.and.pred p, %1, 64, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}\n"
+                : "=r"(both)
+                : "r"(bar), "r"((uint32_t)mine)
+                : "memory");
+            return both != 0;
+        };
         Work cur = take(0);
-        for (uint32_t it = 0; cur.t.g >= 0; ++it) {
+        for (uint32_t it = 0; going(cur.t.g >= 0); ++it) {
             const Work next = take(it + 1);
             const Tile& t = cur.t;
             const uint32_t acc = it & 1u;
@@ -431,7 +457,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int mine = up ? 2 : 0, other = 2 - mine;
                 uint4* give = reinterpret_cast<uint4*>(stage_out) + lane;
                 const uint4* get = reinterpret_cast<const uint4*>(store + (warp - 2 + (up ? 2 : -2)) * kStoreBytes) + lane;
-                const int bar = 1 + 2 * r + (q & 1);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     float v[4][2][2], w[4][2][2];

@@ -9,7 +9,7 @@ from sparse_mixture_experts_stable_b200 import binding as B
 from sparse_mixture_experts_stable_b200.layer import SwiGLUMoEInt8
 from tests.gpu_util import DEV, cpu, cpu64
 from tests.sorted_util import HALF, U, ref_quantize, ref_sort, ref_unsort, routing, within
-from tests.test_gpu_i8 import _ffn_ref
+from tests.test_gpu_i8 import _dev, _ffn_ref, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,25 @@ def test_thousands_of_short_tiles(K, dtype):
     for _ in range(20):
         out = moe.moe_matmul_i8(xq, one[:M], wq, one[:G * N].view(G, N), offsets=off.int(), out_dtype=dtype)
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", ["swiglu", "gelu_mlp"])
+def test_groups_of_every_number_of_rows(kind):
+    """Tiles whose tokens end at every place of the warps that share them; for SwiGLU two warps exchange gate and up."""
+    counts = list(range(70)) + [127, 128, 129, 191, 193, 250, 255, 256, 257, 319, 321, 383, 385, 511, 513]
+    G, D, F, Dout = len(counts), 48, 200, 40
+    off = np.concatenate([[0], np.cumsum(counts)])
+    M = int(off[-1])
+    assert M > 8 * G  # tiles, not the few-row kernel
+    q, s = ref_quantize(torch.randn(M, D, generator=torch.Generator().manual_seed(M)).double().numpy())
+    xq, xs = torch.from_numpy(q).to(torch.int8), torch.from_numpy(s).float()
+    w = _weights(kind, G, D, F, Dout, D)
+    want, bound = _ffn_ref(kind, xq, xs, off, w, F32)
+    status = moe.new_status(DEV)
+    args = _dev(xq), xs.to(DEV), torch.from_numpy(off.astype(np.int32)).to(DEV)
+    wd = {n: _dev(t) for n, t in w.items()}
+    ys = moe.moe_expert_ffn_i8(kind, *args, out_dtype=F32, dev_status=status, **wd)
+    within(cpu64(ys), want, bound, "ys")
+    assert moe.moe_read_status(status) == 0
+    for _ in range(10):
+        assert torch.equal(moe.moe_expert_ffn_i8(kind, *args, out_dtype=F32, **wd), ys)
