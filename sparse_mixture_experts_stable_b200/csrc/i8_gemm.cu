@@ -638,8 +638,12 @@ namespace {
 constexpr size_t kCounterBytes = 256;
 
 bool ffn_sizes_ok(moe_ffn_kind kind, int32_t G, int64_t M, int64_t D, int64_t F, int64_t Dout) {
-    return G >= 1 && M >= 0 && D >= 1 && Dout >= 1 && (kind == MOE_FFN_LINEAR || F >= 1) &&
-           M < (int64_t(1) << 30) && F < (int64_t(1) << 30);
+    return G >= 1 && M >= 0 && D >= 1 && Dout >= 1 && (kind == MOE_FFN_LINEAR || F >= 1);
+}
+
+// in 32 bits, and so that no product of two of them passes 64
+bool ffn_limits_ok(moe_ffn_kind kind, int64_t M, int64_t F, int64_t Dout) {
+    return M < (int64_t(1) << 30) && Dout < (int64_t(1) << 30) && (kind == MOE_FFN_LINEAR || F < (int64_t(1) << 30));
 }
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -666,7 +670,7 @@ extern "C" int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, i
 // workspace: [counters | hscale (M) | hq (M, round16(F)) | h (M, F) fp32]
 extern "C" size_t moe_expert_ffn_i8_workspace_size(moe_ffn_kind kind, int32_t G, int64_t M, int64_t D, int64_t F,
                                                    int64_t Dout) {
-    if (!ffn_sizes_ok(kind, G, M, D, F, Dout) || M == 0) return 0;
+    if (!ffn_sizes_ok(kind, G, M, D, F, Dout) || !ffn_limits_ok(kind, M, F, Dout) || M == 0) return 0;
     if (kind == MOE_FFN_LINEAR) return kCounterBytes;
     return kCounterBytes + align_up((size_t)M * sizeof(float), 256) + align_up((size_t)M * round16(F), 256) +
            (size_t)M * F * sizeof(float);
@@ -681,6 +685,7 @@ extern "C" int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const floa
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     MOE_REQUIRE(kind == MOE_FFN_LINEAR || kind == MOE_FFN_GELU_MLP || kind == MOE_FFN_SWIGLU, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(ffn_sizes_ok(kind, G, M, D, F, Dout), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(ffn_limits_ok(kind, M, F, Dout), MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE(kind != MOE_FFN_SWIGLU || (!b1 && !b2), MOE_ERR_INVALID_ARG);
     if (M == 0) return MOE_OK;
     MOE_REQUIRE(workspace && aligned16(workspace) &&
@@ -695,7 +700,7 @@ extern "C" int moe_expert_ffn_i8(moe_ffn_kind kind, const int8_t* xq, const floa
     }
     // the second product's arguments are checked before the first is enqueued
     MOE_REQUIRE(w2 && s2 && ys && ldw2 >= F && ldys >= Dout && valid_dtype(out_dtype), MOE_ERR_INVALID_ARG);
-    MOE_REQUIRE(aligned16(w2) && ldw2 % 16 == 0 && F <= 131071 && G * Dout < (int64_t(1) << 30) &&
+    MOE_REQUIRE(aligned16(w2) && ldw2 % 16 == 0 && ldw2 < (int64_t(1) << 38) && F <= 131071 && G * Dout < (int64_t(1) << 30) &&
                     reinterpret_cast<uintptr_t>(ys) % dtype_size(out_dtype) == 0,
                 MOE_ERR_UNSUPPORTED);
     uint8_t* ws = static_cast<uint8_t*>(workspace) + kCounterBytes;

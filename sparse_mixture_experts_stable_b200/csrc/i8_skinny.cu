@@ -384,7 +384,7 @@ int launch(const I8Problem& p, cudaStream_t stream) {
 // Groups: SwiGLU experts (E = 256, 2048 x 512, weights in memory) 108 us with 2 rows a group on average (tiles 140), 162 with
 // 8 (175), 198 with 12 (179); (E = 64, 1000 x 200) 27 us with 8 (39), 33 with 16 (42).
 bool i8_skinny_fits(int64_t M, int G, int64_t N, int64_t K) {
-    if (K > kMaxK || G > kMaxG) return false;
+    if (K > kMaxK || G > kMaxG || N >= (int64_t(1) << 30)) return false;  // N: the product below stays in 64 bits
     return G == 1 ? M <= 2048 && M * N * K <= 600000000 : M <= 8 * (int64_t)G;
 }
 

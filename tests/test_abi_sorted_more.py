@@ -3,7 +3,7 @@ import pytest
 
 import sparse_mixture_experts_stable_b200 as moe
 from sparse_mixture_experts_stable_b200 import binding as B
-from tests.test_abi_sorted import BAD, NO, N, P
+from tests.test_abi_sorted import BAD, NO, N, P, ffn, matmul
 
 
 def unsort_ex(L, ys=P, ldys=16, rows=16, dt=0, row=P, g=P, gdt=0, T=8, k=2, n=16, base=N, ldb=0, bdt=0, y=P, ldy=16, ydt=1):
@@ -18,3 +18,25 @@ def unsort_ex(L, ys=P, ldys=16, rows=16, dt=0, row=P, g=P, gdt=0, T=8, k=2, n=16
 ])
 def test_unsort_ex(args, code):
     assert unsort_ex(moe.lib(), **args) == code
+
+
+BIG = 1 << 60  # times 16 it is 0 in 64 bits
+
+
+@pytest.mark.parametrize("call,args,code", [
+    (ffn, dict(G=16, Do=BIG, ldy=BIG), NO), (ffn, dict(kind=1, w3=N, s3=N, G=16, Do=BIG, ldy=BIG), NO),
+    (ffn, dict(kind=0, G=16, Do=BIG, ldy=BIG), NO), (ffn, dict(G=16, F=BIG, ld2=BIG), NO), (ffn, dict(M=1 << 30), NO),
+    (ffn, dict(ld2=1 << 38), NO), (ffn, dict(ld1=1 << 38), NO), (ffn, dict(D=BIG, ldx=BIG, ld1=BIG), NO),
+    (matmul, dict(n=BIG, ldo=BIG), NO), (matmul, dict(M=16, n=BIG, ldo=BIG), NO), (matmul, dict(G=16, off=P, n=BIG, ldo=BIG), NO),
+    (matmul, dict(M=1 << 30), NO), (matmul, dict(M=16, K=BIG, ldx=BIG, ldw=BIG), NO),
+])
+def test_sizes_whose_products_leave_64_bits(call, args, code):
+    assert call(moe.lib(), **args) == code
+
+
+def test_workspace_sizes_beyond_the_limits():
+    for kind in ("swiglu", "gelu_mlp", "linear"):
+        assert B.moe_expert_ffn_i8_workspace_size(kind, 16, 4, 16, 16, BIG) == 0
+        assert B.moe_expert_ffn_i8_workspace_size(kind, 16, 1 << 30, 16, 16, 16) == 0
+    assert B.moe_expert_ffn_i8_workspace_size("swiglu", 16, 4, 16, BIG, 16) == 0
+    assert B.moe_expert_ffn_i8_workspace_size("linear", 16, 4, 16, BIG, 16) > 0  # F is not used
