@@ -735,7 +735,8 @@ def _elsewhere(dev: torch.device, stream) -> bool:
 def _there(dev: torch.device, stream, *tensors):
     """Makes the device, and the stream if given, current; yields the caller's stream if it is another one.
 
-    ``tensors`` (None among them) are the caller's: the allocator waits for the stream before it reuses their memory.
+    ``tensors`` are the caller's: the allocator waits for the stream before it reuses their memory.  What is no CUDA tensor
+    (None, an entry of ``out`` that the call does not know or will refuse) is passed over.
     """
     with torch.cuda.device(dev):
         if stream is None:
@@ -745,7 +746,7 @@ def _there(dev: torch.device, stream, *tensors):
                 raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
             caller = torch.cuda.current_stream(dev)
             for t in tensors:
-                if t is not None:
+                if isinstance(t, torch.Tensor) and t.is_cuda:
                     t.record_stream(stream)
             with torch.cuda.stream(stream):
                 yield caller

@@ -186,3 +186,21 @@ def test_groups_of_every_number_of_rows(kind):
     assert moe.moe_read_status(status) == 0
     for _ in range(10):
         assert torch.equal(moe.moe_expert_ffn_i8(kind, *args, out_dtype=F32, **wd), ys)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_entries_of_out_that_are_no_cuda_tensors(given):
+    """With a stream as without: an entry that the call does not know stays as it is, a wrong one is refused."""
+    stream = torch.cuda.Stream() if given else None
+    sel, x = torch.arange(12, device=DEV).reshape(6, 2) % 4, torch.randn(6, 32, device=DEV)
+    torch.cuda.synchronize()
+    for call, name in ((moe.moe_sort, "xs"), (moe.moe_sort_i8, "xq")):
+        r = call(sel, 4, x, out=dict(note="kept", nothing=None), stream=stream)
+        torch.cuda.synchronize()
+        assert r["note"] == "kept" and r["nothing"] is None and torch.equal(r[name], call(sel, 4, x)[name])
+        for bad in (5, "offsets", torch.zeros(5, dtype=torch.int32), torch.zeros(5, device=DEV)):
+            with pytest.raises((ValueError, TypeError)):
+                call(sel, 4, x, out=dict(offsets=bad), stream=stream)
+        for bad in (5, torch.zeros(12, 32), torch.zeros(12, 32, dtype=torch.float64, device=DEV)):
+            with pytest.raises((ValueError, TypeError)):
+                call(sel, 4, x, out={name: bad}, stream=stream)
