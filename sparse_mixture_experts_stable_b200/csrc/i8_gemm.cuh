@@ -42,8 +42,11 @@ int i8_gemm_run(const I8Problem& p, cudaStream_t stream);
 bool i8_skinny_fits(int64_t M, int G, int64_t N, int64_t K);
 int i8_skinny_run(const I8Problem& p, bool f32x, cudaStream_t stream);
 
-// silu(a) b.  The result is quantised again, so the sigmoid is a full-precision one:
-// an error of 2^-11 (tanh.approx) would move every 90th value across a rounding step.
+// silu(a) b by the fast exponential and quotient.  By CUDA's error tables __expf is off by 2 + 1.173 |a| steps of 2^-23 and
+// __fdividef by 2, so with the sum and the product the result is off by less than (7 + 1.2 |a|) 2^-23 of itself; for a below
+// -87.3, where the exponential passes 2^126, it is 0 instead of a value under 1.1e-36 |b|.  It is quantised to 8 bits next,
+// by steps of 1 / 127 of the row's largest: an error e moves at most one value in 1 / (127 e) across a rounding border, 3400
+// for |a| = 10 (16 with an error of 2^-11, tanh.approx's).
 __device__ __forceinline__ float swiglu_f(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
 
 // Rows of x in 8 bits: all M, or with offsets (G + 1, device) those in [offsets[0], offsets[G]).

@@ -204,3 +204,25 @@ def test_entries_of_out_that_are_no_cuda_tensors(given):
         for bad in (5, torch.zeros(12, 32), torch.zeros(12, 32, dtype=torch.float64, device=DEV)):
             with pytest.raises((ValueError, TypeError)):
                 call(sel, 4, x, out={name: bad}, stream=stream)
+
+
+# 8 rows: the few-row kernel; 2100: tiles
+@pytest.mark.parametrize("M", [8, 2100])
+def test_swiglu_where_the_sigmoid_saturates(M):
+    """Gates from -300 to 300: exp(-gate) from 0 to beyond fp32."""
+    D, F, Dout = 32, 200, 24
+    g = torch.Generator().manual_seed(M)
+    xq = torch.randint(-127, 128, (M, D), generator=g, dtype=torch.int8)
+    xs = torch.full((M,), 1 / 127)
+    w = _weights("swiglu", 1, D, F, Dout, 3)
+    # row f of the gate: +-127 at one place, scaled so that the gate runs from 0 to 300 in size
+    w["w1"] = torch.zeros(1, F, D, dtype=torch.int8)
+    w["w1"][0, torch.arange(F), torch.arange(F) % D] = torch.where(torch.arange(F) % 3 == 0, 127, -127).to(torch.int8)
+    w["s1"] = (torch.arange(F) * 1.5 / 127)[None]
+    off = [0, M]
+    want, bound = _ffn_ref("swiglu", xq, xs, off, w, F32)
+    status = moe.new_status(DEV)
+    ys = moe.moe_expert_ffn_i8("swiglu", _dev(xq), xs.to(DEV), None, out_dtype=F32, dev_status=status,
+                               **{n: _dev(t) for n, t in w.items()})
+    assert moe.moe_read_status(status) == 0 and torch.isfinite(ys).all()
+    within(cpu64(ys), want, bound, "ys")
