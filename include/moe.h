@@ -517,7 +517,9 @@ MOE_API int moe_quantize_i8(const void* x, moe_dtype dtype, int64_t M, int64_t K
  *             G = 1) on a 16-byte boundary, one per call in flight.
  * xq and wq start on 16 bytes with row strides of multiples of 16 (K itself is
  * free), else MOE_ERR_UNSUPPORTED.  G <= 2048, K <= 131071 (the int32 sum),
- * M and G N below 2^30.  M = 0: nothing is done.
+ * M and G N below 2^30.  M = 0: nothing is done.  Few rows (up to 8 per group on
+ * average, or a small dense product) have a kernel of their own where K <= 4096
+ * and G <= 1024; beyond that a call of few rows takes several times longer.
  */
 MOE_API size_t moe_matmul_i8_workspace_size(int64_t M, int32_t G, int64_t N, int64_t K);
 MOE_API int moe_matmul_i8(const int8_t* xq, const float* xscale, int64_t M, int64_t ldx, const int32_t* offsets,

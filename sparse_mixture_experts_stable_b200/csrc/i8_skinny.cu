@@ -383,6 +383,13 @@ int launch(const I8Problem& p, cudaStream_t stream) {
 // Where this kernel is the faster one.  One group: N = K = 2048 13.1 us at 128 rows, as the tiles, 9.7 at 64 (tiles 20).
 // Groups: SwiGLU experts (E = 256, 2048 x 512, weights in memory) 108 us with 2 rows a group on average (tiles 140), 162 with
 // 8 (175), 198 with 12 (179); (E = 64, 1000 x 200) 27 us with 8 (39), 33 with 16 (42).
+// The rule knows the mean only, and a full group has its weights read once per kTok rows: G + M / kTok blocks of weights in
+// all at most, half as many again as a balanced call's (K > 2048: twice as many), and fewer groups' from memory.  All rows in one of 256 groups of 2048 x 512: 256 rows 8 us (tiles 15), 1024 17 (15), 2048 28
+// (17); balanced 55 (66); half of 2048 in one 65 (69).  1024 groups of 2048 x 2048, 8192 rows: in one 305 us (45), balanced
+// 635 (748), half in one 728 (752).
+// kMaxK: the tokens' rows lie whole in shared memory beside the ring (33 KB for 8 of 4096).  One row times 2048 x 4096 6 us,
+// 2048 x 4112 (tiles, of which 8 pairs have one) 19, 2048 x 8192 31, 4096 x 14336 49.  kMaxG: the groups' tables; 8 rows each
+// of 1024 groups of 512 x 512 61 us, of 1025 (tiles) 69.
 bool i8_skinny_fits(int64_t M, int G, int64_t N, int64_t K) {
     if (K > kMaxK || G > kMaxG || N >= (int64_t(1) << 30)) return false;  // N: the product below stays in 64 bits
     return G == 1 ? M <= 2048 && M * N * K <= 600000000 : M <= 8 * (int64_t)G;

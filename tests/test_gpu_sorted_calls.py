@@ -226,3 +226,22 @@ def test_swiglu_where_the_sigmoid_saturates(M):
                                **{n: _dev(t) for n, t in w.items()})
     assert moe.moe_read_status(status) == 0 and torch.isfinite(ys).all()
     within(cpu64(ys), want, bound, "ys")
+
+
+# 1024 rows in 256 groups: 4 on average, so the few-row kernel takes them, whatever their distribution; at a real size
+@pytest.mark.parametrize("full", [1024, 512, 17])
+@pytest.mark.parametrize("N,K", [(2048, 512), (512, 2048)])
+def test_one_very_full_expert_in_the_few_row_kernel(full, N, K):
+    G, M = 256, 1024
+    gen = torch.Generator(device=DEV).manual_seed(full)
+    counts = torch.bincount(torch.randint(0, G, (M - full,), device=DEV, generator=gen), minlength=G)
+    counts[77] += full
+    off = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    xq = torch.randint(-128, 128, (M, K), device=DEV, generator=gen).to(torch.int8)
+    wq = torch.randint(-128, 128, (G, N, K), device=DEV, generator=gen).to(torch.int8)
+    xs, ws = (torch.rand(n, device=DEV, generator=gen) + 0.5 for n in (M, G * N))
+    out = moe.moe_matmul_i8(xq, xs, wq, ws.view(G, N), offsets=off.int(), out_dtype=F32)
+    for g in counts.nonzero().flatten().tolist():
+        a, b = int(off[g]), int(off[g + 1])
+        want = (xq[a:b].double() @ wq[g].double().T) * xs[a:b, None].double() * ws.view(G, N)[g].double()
+        assert ((out[a:b].double() - want).abs() <= 3.01 * U * want.abs()).all()  # to fp32, and the two scales
