@@ -9,7 +9,7 @@ from sparse_mixture_experts_stable_b200 import binding as B
 from sparse_mixture_experts_stable_b200.layer import SwiGLUMoEInt8
 from tests.gpu_util import DEV, cpu, cpu64
 from tests.sorted_util import HALF, U, ref_quantize, ref_sort, ref_unsort, routing, within
-from tests.test_gpu_i8 import _dev, _ffn_ref, _weights
+from tests.test_gpu_i8 import _dev, _ffn_ref, _i8, _product, _scale, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +245,68 @@ def test_one_very_full_expert_in_the_few_row_kernel(full, N, K):
         a, b = int(off[g]), int(off[g + 1])
         want = (xq[a:b].double() @ wq[g].double().T) * xs[a:b, None].double() * ws.view(G, N)[g].double()
         assert ((out[a:b].double() - want).abs() <= 3.01 * U * want.abs()).all()  # to fp32, and the two scales
+
+
+def _not_finite(D, dtype):
+    """(column, value): infinities and NaNs of both signs, with the smallest and the largest payload, over the row's ends."""
+    bits = torch.tensor([0x7f800000, -0x800000, 0x7f800001 if dtype is F32 else 0x7f810000, -1], dtype=torch.int32)
+    return list(zip([0, D - 1, D // 2, D - 1], bits.view(F32).to(dtype) if dtype is F32 else
+                    (bits >> 16).to(torch.int16).view(BF16)))
+
+
+def _check_not_finite(x, bad):
+    """x's rows bad[i] get the values; returns what each row must be."""
+    D = x.shape[1]
+    q, s = ref_quantize(cpu64(x))
+    for i, (col, v) in zip(bad, _not_finite(D, x.dtype)):
+        x[i, col] = v
+        q[i], s[i] = 0, np.nan
+    assert not torch.isfinite(x[bad].float()).all(1).any()
+    return q, s.astype(np.float32)
+
+
+# teams of 1, 2, 4 and 8 warps, a block per row: few rows of a team's width, and wider ones
+@pytest.mark.parametrize("M,steps", [(1300, 3.5), (1300, 7), (700, 13.25), (400, 30.5), (40, 30.5), (400, 41)])
+@pytest.mark.parametrize("dtype,step", [(F32, 128), (BF16, 256)])
+def test_quantize_reports_rows_that_are_not_finite_at_every_width(M, steps, dtype, step):
+    x = torch.randn(M, int(steps * step), generator=torch.Generator().manual_seed(M)).to(dtype)
+    q, s = _check_not_finite(x, [3, M // 2, M - 2, M - 1])
+    status = moe.new_status(DEV)
+    got, scale = moe.moe_quantize_i8(x.to(DEV), dev_status=status)
+    assert moe.moe_read_status(status) == B.MOE_ERR_NONFINITE
+    np.testing.assert_array_equal(cpu(got), q)
+    np.testing.assert_array_equal(cpu(scale), s)
+
+
+@pytest.mark.parametrize("T,k,steps,skip", ROW_KERNELS)
+@pytest.mark.parametrize("dtype,step", [(F32, 128), (BF16, 256)])
+def test_sort_i8_reports_rows_that_are_not_finite_at_every_width(T, k, steps, skip, dtype, step):
+    D, E = int(steps * step), 24
+    sel = routing(np.random.default_rng(T + D), T, k, E)
+    _, row, _ = ref_sort(sel, E)
+    x = torch.randn(T, D, generator=torch.Generator().manual_seed(D)).to(dtype)
+    q, s = _check_not_finite(x, [3, T // 2, T - 2, T - 1])
+    status = moe.new_status(DEV)
+    r = _sort_i8_at(torch.from_numpy(sel).to(DEV), E, x.to(DEV), skip, status)
+    assert moe.moe_read_status(status) == B.MOE_ERR_NONFINITE
+    t, j = np.nonzero(row >= 0)
+    np.testing.assert_array_equal(cpu(r["xq"])[row[t, j]], q[t])
+    np.testing.assert_array_equal(cpu(r["xscale"])[row[t, j]], s[t])
+
+
+# 12 rows per group on average: tiles; 4: the few-row kernel
+@pytest.mark.parametrize("G", [4, 12])
+def test_every_row_under_offsets_that_run_backwards(G):
+    """The rows that two groups claim belong to the first, as the running maximum of the offsets says."""
+    M, K, N = 50, 64, 40
+    xq, wq, xs, ws = _i8((M, K), 1), _i8((G, N, K), 2), _scale((M,), 3), _scale((G, N), 4)
+    raw = [-5, 10, 4, 30] + [2 ** 31 - 1] * (G - 3)
+    status = moe.new_status(DEV)
+    out = torch.full((M + 1, N), 7.0, device=DEV)
+    moe.moe_matmul_i8(_dev(xq), xs.to(DEV), _dev(wq), ws.to(DEV), out=out[:M], dev_status=status,
+                      offsets=torch.tensor(raw, dtype=torch.int32, device=DEV))
+    assert moe.moe_read_status(status) == B.MOE_ERR_BAD_INDEX
+    want, bound, written = _product(xq, xs, wq, ws, None, [0, 10, 10, 30] + [M] * (G - 3), F32)
+    assert written.all()
+    within(cpu64(out)[:M], want, bound, "out")
+    assert (out[M] == 7).all()
