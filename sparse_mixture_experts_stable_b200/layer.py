@@ -169,8 +169,18 @@ class SwiGLUMoEInt8:
     def forward(self, x, w_router, router_bias, experts, shared=None):
         """x (T,H); w_router (E,H); ``experts`` and ``shared`` (the latter with E = 1) from ``quantize``.
 
-        The shared expert runs on a second stream, as in SwiGLUMoE.
+        The shared expert runs on a second stream, as in SwiGLUMoE.  The buffers are made for T tokens of the layer's type:
+        others are refused.
         """
+        for name, t, shape, dtype in (("x", x, (self.T, self.H), self.dtype), ("w_router", w_router, (self.E, self.H), self.dtype),
+                                      ("router_bias", router_bias, (self.E,), None)):
+            if t is None and name == "router_bias":
+                continue
+            if t.shape != shape or t.device != self.y.device or (dtype is not None and t.dtype is not dtype):
+                raise ValueError(f"{name} must be {shape}, {dtype or 'any float'}, on {self.y.device}; got {tuple(t.shape)}, "
+                                 f"{t.dtype}, on {t.device}")
+        if self.F_shared and shared is None:
+            raise ValueError("the layer has a shared expert")
         main = torch.cuda.current_stream(x.device)
         base = None
         if self.F_shared:

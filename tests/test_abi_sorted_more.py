@@ -1,8 +1,10 @@
 """More refusals of the sorted-row and 8-bit entry points, on the CPU: no kernel is launched, no pointer is read."""
 import pytest
+import torch
 
 import sparse_mixture_experts_stable_b200 as moe
 from sparse_mixture_experts_stable_b200 import binding as B
+from sparse_mixture_experts_stable_b200.layer import SwiGLUMoEInt8
 from tests.test_abi_sorted import BAD, NO, N, P, ffn, matmul
 
 
@@ -40,3 +42,17 @@ def test_workspace_sizes_beyond_the_limits():
         assert B.moe_expert_ffn_i8_workspace_size(kind, 16, 1 << 30, 16, 16, 16) == 0
     assert B.moe_expert_ffn_i8_workspace_size("swiglu", 16, 4, 16, BIG, 16) == 0
     assert B.moe_expert_ffn_i8_workspace_size("linear", 16, 4, 16, BIG, 16) > 0  # F is not used
+
+
+def test_the_layer_takes_what_its_buffers_were_made_for():
+    """The router writes T rows of x's type into the layer's buffers, so others are refused before it is called."""
+    T, H, E = 6, 32, 4
+    x, wr, b = torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(E, H, dtype=torch.bfloat16), torch.zeros(E)
+    layer = SwiGLUMoEInt8(T, H, E, 16, 2, device="cpu")
+    for name, args in (("x", (x[:5], wr, b)), ("x", (x.repeat(2, 1), wr, b)), ("x", (x[:, :16], wr, b)), ("x", (x.float(), wr, b)),
+                       ("x", (x.to("meta"), wr, b)), ("w_router", (x, wr.repeat(2, 1), b)), ("w_router", (x, wr.float(), b)),
+                       ("w_router", (x, wr[:, :16], b)), ("router_bias", (x, wr, b[:3])), ("router_bias", (x, wr, b.to("meta")))):
+        with pytest.raises(ValueError, match=f"^{name} must be"):
+            layer.forward(*args, experts={})
+    with pytest.raises(ValueError, match="shared expert"):
+        SwiGLUMoEInt8(T, H, E, 16, 2, F_shared=16, device="cpu").forward(x, wr, b, {})
