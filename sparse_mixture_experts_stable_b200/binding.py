@@ -944,7 +944,7 @@ def moe_unsort(ys: torch.Tensor, row: torch.Tensor, gates: Optional[torch.Tensor
 
     ``ys`` (rows, N); ``row`` int32 (T, k) from ``moe_sort``; without gates the sum is the gradient of ``moe_sort``.
     y has ys's type, or bf16 (``out_dtype``, or the given y's) where ys is fp32: the sum is then the only rounding, by
-    ``moe_unsort_ex``.  base has the type of ys or of y.
+    ``moe_unsort_ex``.  base has the type of ys or of y.  ``moe_unsort_backward`` takes dy in ys's type.
     """
     dev = _dev(ys)
     if ys.dim() != 2:
@@ -1200,7 +1200,8 @@ def moe_expert_ffn_i8(kind: str, xq: torch.Tensor, xscale: torch.Tensor, offsets
 
     ``xq``, ``xscale`` and ``offsets`` from ``moe_sort_i8``; weights int8 (G, out, in) with one scale per output channel
     from ``moe_quantize_i8`` (swiglu: w1 = gate, w3 = up, w2 = down); biases fp32 (G, out).  The hidden rows are quantised
-    from fp32 between the two products.
+    from fp32 between the two products.  ys is bf16 unless ``out_dtype`` says fp32, which ``moe_unsort`` sums into bf16 with
+    one rounding.
     """
     if kind not in FFN:
         raise ValueError(f"unknown kind {kind!r}; known: {sorted(FFN)}")
