@@ -174,8 +174,8 @@ class SwiGLUMoEInt8:
         """
         for name, t, shape, dtype in (("x", x, (self.T, self.H), self.dtype), ("w_router", w_router, (self.E, self.H), self.dtype),
                                       ("router_bias", router_bias, (self.E,), None)):
-            if t is None and name == "router_bias":
-                continue
+            if name == "router_bias" and (t is None or t.numel() == self.E and t.device == self.y.device):
+                continue  # any shape of E values
             if t.shape != shape or t.device != self.y.device or (dtype is not None and t.dtype is not dtype):
                 raise ValueError(f"{name} must be {shape}, {dtype or 'any float'}, on {self.y.device}; got {tuple(t.shape)}, "
                                  f"{t.dtype}, on {t.device}")

@@ -310,3 +310,20 @@ def test_every_row_under_offsets_that_run_backwards(G):
     assert written.all()
     within(cpu64(out)[:M], want, bound, "out")
     assert (out[M] == 7).all()
+
+
+def test_layer_biases():
+    """No router bias, and E values of any shape."""
+    T, H, E, F = 9, 64, 8, 32
+    g = torch.Generator().manual_seed(2)
+    mk = lambda *s: (torch.randn(*s, generator=g) * 0.1).to(BF16).to(DEV)  # noqa: E731
+    x, wr, experts = mk(T, H), mk(E, H), SwiGLUMoEInt8.quantize(mk(E, F, H), mk(E, F, H), mk(E, H, F))
+    layer = SwiGLUMoEInt8(T, H, E, F, 2)
+    run = lambda bias: layer.forward(x, wr, bias, experts)["y"].clone()  # noqa: E731
+    bias = torch.randn(E, device=DEV)
+    assert torch.equal(run(None), run(torch.zeros(E, device=DEV)))
+    assert torch.equal(run(bias), run(bias[None]))
+    for bad in (bias[:3], bias.cpu()):
+        with pytest.raises(ValueError):
+            run(bad)
+    assert moe.moe_read_status(layer.status) == 0
